@@ -367,6 +367,172 @@ size_t kvc_attend_workspace_bytes(const kvc_attn_desc *attn);
 kvc_status kvc_attend(const void *in, size_t in_bytes, const kvc_attn_desc *attn,
                       void *workspace, size_t workspace_bytes, kvc_stream_t stream);
 
+/* ---- A paged cache that stays in 4 bits (the pages stop at the decode
+ * GPU's decompression; the ZipFusion abstract on the first page reads a
+ * compressed cache in place, but its stream takes no new token).
+ *
+ * On the decode GPU a compressed cache has to grow by a token per step. These
+ * four calls keep it as pages of the codec's own codes: kvc_cache_load puts
+ * a received stream's codes into pages as they are (nothing is decoded or
+ * quantised again), kvc_cache_write quantises new tokens into their slots,
+ * kvc_cache_attend reads the pages for decode, verification and prompt
+ * chunks, kvc_cache_read gives stored rows back. A vector written here has the
+ * codes and meta that kvc_compress gives it, bit for bit.
+ *
+ * Inference only: stored codes are integers, no gradient passes through them.
+ *
+ * Pool layout. `pool` holds a block per (layer, page, kv, head) at
+ *   pool + l*stride_layer + p*stride_page + kv*stride_kv + h*stride_head
+ * (bytes). A block holds page_tokens / 16 tiles of 16 tokens, one after
+ * another; a tile is the 16 tokens' codes (head_dim / 2 bytes each), then their
+ * meta (head_dim / group_size words each: fp16 scale, fp16 zero, both x 2^-3).
+ * A code row is the stream's (channel order, low nibble first) with a key's
+ * 4-byte words, in order [head_dim / 32][4], stored as [4][head_dim / 32], and
+ * a value's 2-byte halfwords, in order [head_dim / 32][8], as
+ * [8][head_dim / 32]: the order in which the attention's lanes take them.
+ * kvc_cache_block_bytes gives a block's size. Slot s of a page p is slot
+ * number p * page_tokens + s.
+ *
+ * Status. These calls do not clear the status word that they are given
+ * (DEVICE, 4 bytes, 4-byte aligned, may be null): one word collects the first
+ * data-dependent error of a whole step's calls over many layers. Clear it
+ * with kvc_cache_status_clear, read it with kvc_stream_status.
+ *
+ * Concurrency. Calls that write the same slots, or share a workspace, must
+ * not overlap (two captured graphs included). All pointers belong to the
+ * current device. Every call can be captured in a CUDA graph: lengths, page
+ * tables and slots are read on the device at each replay; the counts given on
+ * the host are fixed. */
+enum { KVC_BF16 = 0, KVC_FP16 = 1 };
+
+typedef struct {
+  int32_t layers;
+  int32_t kv_heads;
+  int32_t head_dim;           /* 64 or 128 */
+  int32_t bits;               /* 4 */
+  int32_t group_size;         /* 32, 64 or 128, dividing head_dim */
+  int32_t quant;              /* KVC_QUANT_ASYM or KVC_QUANT_SYM (of writes; both
+                                 read alike) */
+  int32_t signs;              /* KVC_SIGNS_* */
+  int32_t first_layer;        /* >= 0: layer l of this description takes the
+                                 per-vector diagonals of layer first_layer + l */
+  uint64_t sign_seed;
+  int32_t page_tokens;        /* a multiple of 16, 16 .. 65536 */
+  int32_t reserved;           /* 0 */
+  int64_t num_pages;          /* 0 .. 2^31 - 1 */
+  void *pool;                 /* DEVICE, 16-byte aligned */
+  int64_t stride_layer;       /* bytes, multiples of 16 */
+  int64_t stride_page;
+  int64_t stride_kv;
+  int64_t stride_head;
+} kvc_cache_desc;
+
+/* Bytes of one (layer, page, kv, head) block; 0 for an invalid description
+ * (the pool and its strides are not looked at). */
+size_t kvc_cache_block_bytes(const kvc_cache_desc *cache);
+
+/* Rows of new or stored tokens: element (l, i, h, c) of k at k +
+ * l*k_stride_layer + i*k_stride_token + h*k_stride_head + c, v alike, in
+ * elements; strides are multiples of 8, vector starts 16-byte aligned. */
+typedef struct {
+  int32_t dtype;              /* KVC_BF16 or KVC_FP16 */
+  int32_t reserved;           /* 0 */
+  int64_t tokens;             /* 0 .. 2^31 - 1 */
+  void *k;                    /* DEVICE [layers][tokens][kv_heads][head_dim] */
+  void *v;
+  int64_t k_stride_layer, k_stride_token, k_stride_head;
+  int64_t v_stride_layer, v_stride_token, v_stride_head;
+  const int64_t *slots;       /* DEVICE [tokens], 8-byte aligned; a negative
+                                 slot skips its token */
+} kvc_cache_rows;
+
+/* Quantises rows->k and rows->v (read only) into their slots, in every layer
+ * and head of the description. The slots of one call must differ; a slot
+ * named twice holds a mixture of its rows. A vector that transforms to inf or
+ * NaN (KVC_ERR_NONFINITE), or whose scale or zero overflows fp16
+ * (KVC_ERR_RANGE), is stored with NaN scales, so that whatever reads it gives
+ * NaN; other rows are not affected. A slot outside the pool sets
+ * KVC_ERR_CORRUPT and its token is skipped. One kernel. */
+kvc_status kvc_cache_write(const kvc_cache_desc *cache, const kvc_cache_rows *rows,
+                           uint32_t *status, kvc_stream_t stream);
+
+/* The stored rows of rows->slots, inverse transform included, rounded once to
+ * dtype, into rows->k and rows->v. Values past fp16's range become infinite.
+ * Rows with a negative slot are left as they were; a slot outside the pool
+ * sets KVC_ERR_CORRUPT and its rows are left as they were. Slots may repeat.
+ * One kernel. */
+kvc_status kvc_cache_read(const kvc_cache_desc *cache, const kvc_cache_rows *rows,
+                          uint32_t *status, kvc_stream_t stream);
+
+/* Puts the codes and meta of the compressed stream `in` into the cache: the
+ * vectors of the stream's token t (requests concatenated in order, as
+ * kvc_compress codes them) go to slots[t] (DEVICE, [sum of seq_lens]; negative:
+ * the token is skipped). The stream must describe layers x kv_heads x
+ * head_dim vectors of these requests, 4-bit ASYM or SYM codes of this group
+ * size, the same sign mode and the same diagonals (with per-vector diagonals
+ * and first_layer > 0: a stream of those layers alone whose seed is the one
+ * whose diagonal 0 is theirs, see kvc_cache_stream_seed), and store its code
+ * chunks raw, as kvc_attend asks; else KVC_ERR_CORRUPT, and the slots' content
+ * is unspecified. Here the status word is the workspace's (cleared by the
+ * call). seq_lens: HOST. */
+size_t kvc_cache_load_workspace_bytes(const kvc_cache_desc *cache, const int32_t *seq_lens,
+                                      int32_t n_requests);
+kvc_status kvc_cache_load(const void *in, size_t in_bytes, const kvc_cache_desc *cache,
+                          const int32_t *seq_lens, int32_t n_requests, const int64_t *slots,
+                          void *workspace, size_t workspace_bytes, kvc_stream_t stream);
+
+/* The sign seed with which a stream of this description's layers alone has the
+ * description's diagonals (pass it as kvc_params.sign_seed): sign_seed itself
+ * unless signs is KVC_SIGNS_PER_VECTOR and first_layer > 0. */
+uint64_t kvc_cache_stream_seed(const kvc_cache_desc *cache);
+
+/* Attention of query tokens over the requests' pages. Request r has the
+ * seq_lens[r] tokens of its row of the page table (token t in slot t %
+ * page_tokens of page page_table[r*page_table_stride + t/page_tokens]) and the
+ * query tokens q_starts[r] .. q_starts[r+1] - 1 of q (null q_starts: token r
+ * only). Query i of n stands at position seq_lens[r] - n + i: its own key is in
+ * the cache already (write first, then attend). It sees the keys
+ *   t <= position if causal, all seq_lens[r] otherwise; and t > position -
+ *   window if window > 0 (causal only).
+ * Query head j reads kv head j / q_per_kv:
+ *   s_t = scale * q . k_t,  out = sum_t softmax(s)_t v_t,  lse = ln sum_t e^s_t
+ * with k_t, v_t the stored vectors before kvc_cache_read's rounding. Scores and
+ * sums are held in fp32, out is rounded once to dtype. A query that sees no key
+ * gives zeros and lse -inf. Rows of q that no request names are left as they
+ * were in out and lse; NaN and infinities in slots past a request's length are
+ * never used. A request whose q_starts or seq_lens is out of range (decreasing
+ * or outside [0, q_tokens]; more than max_q queries; a length below 0 or past
+ * its row of the page table) sets KVC_ERR_CORRUPT and its rows are left as they
+ * were; a page outside the pool sets it too and the page's tokens are left out. */
+#define KVC_CACHE_MAX_Q_PER_KV 64
+typedef struct {
+  int32_t dtype;              /* KVC_BF16 or KVC_FP16, of q and out */
+  int32_t q_per_kv;           /* 1 .. KVC_CACHE_MAX_Q_PER_KV */
+  int32_t n_requests;         /* 0 .. KVC_MAX_REQUESTS */
+  int32_t max_q;              /* >= 1: query tokens of one request at most */
+  int32_t causal;             /* 0 or 1 */
+  int32_t window;             /* 0: none */
+  float scale;
+  int32_t reserved;           /* 0 */
+  int64_t q_tokens;           /* rows of q, 0 .. 2^24 */
+  const int32_t *q_starts;    /* DEVICE [n_requests + 1], or null */
+  const int32_t *seq_lens;    /* DEVICE [n_requests] */
+  const int32_t *page_table;  /* DEVICE [n_requests][page_table_stride] */
+  int64_t page_table_stride;
+  const void *q;              /* DEVICE [layers][q_tokens][kv_heads * q_per_kv][head_dim] */
+  int64_t q_stride_layer, q_stride_token, q_stride_head;  /* elements, multiples of 8 */
+  void *out;                  /* DEVICE, as q */
+  int64_t out_stride_layer, out_stride_token, out_stride_head;
+  float *lse;                 /* DEVICE fp32 [layers][q_tokens][heads], contiguous, or null */
+} kvc_cache_attn;
+size_t kvc_cache_attend_workspace_bytes(const kvc_cache_desc *cache, const kvc_cache_attn *attn);
+kvc_status kvc_cache_attend(const kvc_cache_desc *cache, const kvc_cache_attn *attn,
+                            void *workspace, size_t workspace_bytes, uint32_t *status,
+                            kvc_stream_t stream);
+
+/* Sets the status word to KVC_OK on `stream`. */
+kvc_status kvc_cache_status_clear(uint32_t *status, kvc_stream_t stream);
+
 /* Measurement only (no page defines these; they let a benchmark time each
  * kernel of a call with CUDA events on the call's own stream). The same work
  * and results as kvc_compress / kvc_decompress, with n_events == 5 caller-

@@ -30,7 +30,10 @@ EXPORTS = ["kvc_max_compressed_bytes", "kvc_workspace_bytes", "kvc_compress",
            "kvc_decompress_workspace_bytes", "kvc_unfused_workspace_bytes",
            "kvc_compress_unfused", "kvc_test_compress_stalled", "kvc_compress_timed",
            "kvc_decompress_timed", "kvc_attend_workspace_bytes", "kvc_attend",
-           "kvc_attend_timed", "kvc_test_e2m1", "kvc_test_div_const",
+           "kvc_attend_timed", "kvc_cache_block_bytes", "kvc_cache_stream_seed",
+           "kvc_cache_status_clear", "kvc_cache_write", "kvc_cache_read",
+           "kvc_cache_load_workspace_bytes", "kvc_cache_load",
+           "kvc_cache_attend_workspace_bytes", "kvc_cache_attend", "kvc_test_e2m1", "kvc_test_div_const",
            "kvc_test_rcp_scale"]
 
 
@@ -61,6 +64,41 @@ class kvc_attn_desc(C.Structure):
                 ("quant", C.c_int32), ("kernel", C.c_int32), ("n_requests", C.c_int32),
                 ("scale", C.c_float),
                 ("seq_lens", C.POINTER(C.c_int32)), ("q", C.c_void_p), ("out", C.c_void_p)]
+
+
+# Element types of the paged cache's rows, queries and outputs.
+KVC_BF16, KVC_FP16 = 0, 1
+KVC_CACHE_MAX_Q_PER_KV = 64
+
+
+class kvc_cache_desc(C.Structure):
+    _fields_ = [("layers", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("bits", C.c_int32), ("group_size", C.c_int32), ("quant", C.c_int32),
+                ("signs", C.c_int32), ("first_layer", C.c_int32), ("sign_seed", C.c_uint64),
+                ("page_tokens", C.c_int32), ("reserved", C.c_int32), ("num_pages", C.c_int64),
+                ("pool", C.c_void_p), ("stride_layer", C.c_int64), ("stride_page", C.c_int64),
+                ("stride_kv", C.c_int64), ("stride_head", C.c_int64)]
+
+
+class kvc_cache_rows(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("reserved", C.c_int32), ("tokens", C.c_int64),
+                ("k", C.c_void_p), ("v", C.c_void_p),
+                ("k_stride_layer", C.c_int64), ("k_stride_token", C.c_int64),
+                ("k_stride_head", C.c_int64), ("v_stride_layer", C.c_int64),
+                ("v_stride_token", C.c_int64), ("v_stride_head", C.c_int64),
+                ("slots", C.c_void_p)]
+
+
+class kvc_cache_attn(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("q_per_kv", C.c_int32), ("n_requests", C.c_int32),
+                ("max_q", C.c_int32), ("causal", C.c_int32), ("window", C.c_int32),
+                ("scale", C.c_float), ("reserved", C.c_int32), ("q_tokens", C.c_int64),
+                ("q_starts", C.c_void_p), ("seq_lens", C.c_void_p), ("page_table", C.c_void_p),
+                ("page_table_stride", C.c_int64), ("q", C.c_void_p),
+                ("q_stride_layer", C.c_int64), ("q_stride_token", C.c_int64),
+                ("q_stride_head", C.c_int64), ("out", C.c_void_p),
+                ("out_stride_layer", C.c_int64), ("out_stride_token", C.c_int64),
+                ("out_stride_head", C.c_int64), ("lse", C.c_void_p)]
 
 
 class kvc_kv_desc(C.Structure):
@@ -125,6 +163,22 @@ def lib() -> C.CDLL:
         L.kvc_attend_timed.restype = C.c_int
         L.kvc_attend_timed.argtypes = [C.c_void_p, C.c_size_t, A, C.c_void_p, C.c_size_t,
                                        C.POINTER(C.c_void_p), C.c_int, C.c_void_p]
+        K, R, T = C.POINTER(kvc_cache_desc), C.POINTER(kvc_cache_rows), C.POINTER(kvc_cache_attn)
+        for name, res, args in (
+                ("kvc_cache_block_bytes", C.c_size_t, [K]),
+                ("kvc_cache_stream_seed", C.c_uint64, [K]),
+                ("kvc_cache_status_clear", C.c_int, [C.c_void_p, C.c_void_p]),
+                ("kvc_cache_write", C.c_int, [K, R, C.c_void_p, C.c_void_p]),
+                ("kvc_cache_read", C.c_int, [K, R, C.c_void_p, C.c_void_p]),
+                ("kvc_cache_load_workspace_bytes", C.c_size_t, [K, C.POINTER(C.c_int32), C.c_int32]),
+                ("kvc_cache_load", C.c_int, [C.c_void_p, C.c_size_t, K, C.POINTER(C.c_int32),
+                                             C.c_int32, C.c_void_p, C.c_void_p, C.c_size_t,
+                                             C.c_void_p]),
+                ("kvc_cache_attend_workspace_bytes", C.c_size_t, [K, T]),
+                ("kvc_cache_attend", C.c_int, [K, T, C.c_void_p, C.c_size_t, C.c_void_p,
+                                               C.c_void_p])):
+            getattr(L, name).restype = res
+            getattr(L, name).argtypes = args
         L.kvc_test_e2m1.restype = C.c_int
         L.kvc_test_e2m1.argtypes = [C.c_void_p, C.c_void_p, C.c_uint64, C.c_void_p]
         L.kvc_test_div_const.restype = C.c_int
@@ -241,6 +295,46 @@ def kvc_status_string(status: int) -> str:
     return lib().kvc_status_string(status).decode()
 
 
+def kvc_cache_block_bytes(cache: kvc_cache_desc) -> int:
+    return lib().kvc_cache_block_bytes(C.byref(cache))
+
+
+def kvc_cache_stream_seed(cache: kvc_cache_desc) -> int:
+    return lib().kvc_cache_stream_seed(C.byref(cache))
+
+
+def kvc_cache_status_clear(status_ptr, stream) -> int:
+    return lib().kvc_cache_status_clear(status_ptr, stream)
+
+
+def kvc_cache_write(cache, rows, status_ptr, stream) -> int:
+    return lib().kvc_cache_write(C.byref(cache), C.byref(rows), status_ptr, stream)
+
+
+def kvc_cache_read(cache, rows, status_ptr, stream) -> int:
+    return lib().kvc_cache_read(C.byref(cache), C.byref(rows), status_ptr, stream)
+
+
+def kvc_cache_load_workspace_bytes(cache, seq_lens) -> int:
+    arr = (C.c_int32 * max(len(seq_lens), 1))(*seq_lens)
+    return lib().kvc_cache_load_workspace_bytes(C.byref(cache), arr, len(seq_lens))
+
+
+def kvc_cache_load(in_ptr, in_bytes, cache, seq_lens, slots_ptr, ws_ptr, ws_bytes, stream) -> int:
+    arr = (C.c_int32 * max(len(seq_lens), 1))(*seq_lens)
+    return lib().kvc_cache_load(in_ptr, in_bytes, C.byref(cache), arr, len(seq_lens), slots_ptr,
+                                ws_ptr, ws_bytes, stream)
+
+
+def kvc_cache_attend_workspace_bytes(cache, attn) -> int:
+    return lib().kvc_cache_attend_workspace_bytes(C.byref(cache), C.byref(attn))
+
+
+def kvc_cache_attend(cache, attn, ws_ptr, ws_bytes, status_ptr, stream) -> int:
+    return lib().kvc_cache_attend(C.byref(cache), C.byref(attn), ws_ptr, ws_bytes, status_ptr,
+                                  stream)
+
+
 # ------------------------------------------------------- descriptor helpers --
 def params(bits: int, group: int, sign_seed: int = 0, lossless: int = KVC_LOSSLESS_FIXED,
            quant: int = KVC_QUANT_ASYM, signs: int = KVC_SIGNS_GLOBAL) -> kvc_params:
@@ -337,3 +431,212 @@ class Codec:
         _check(st, "kvc_decompress")
         if check:
             _check(kvc_stream_status(ws.data_ptr(), _stream_ptr(stream)), "kvc_decompress (device)")
+
+
+def _strides(t):
+    """Strides of all dimensions but the last; those that are never stepped along, 0."""
+    return [st if n > 1 else 0 for n, st in zip(t.shape[:-1], t.stride())]
+
+
+class PagedCache:
+    """A KV cache that stays in 4-bit pages on the decode GPU (kvc_cache_* in
+    include/kvc.h): ``load`` a received stream, ``write`` new tokens, ``attend``
+    over the pages, ``read`` rows back.
+
+    ``pool`` is a uint8 tensor [layers, num_pages, 2, kv_heads, block] (any
+    strides but the last, which is 1; made here if not given). ``cache[i]`` and
+    ``cache[a:b]`` are views of some layers; rows and queries always have a
+    leading layer dimension of that length. Slot numbers are page * page_tokens
+    + place in the page.
+
+    Calls are asynchronous on the current stream (or ``stream``). Errors in
+    arguments raise at once; data-dependent errors collect in one status word,
+    shared by all views, which ``check`` reads (it waits) and clears. Buffers come
+    from PyTorch's caching allocator: a workspace grows to the largest call seen
+    on its stream and is kept, outside of a graph capture."""
+
+    def __init__(self, layers: int, kv_heads: int, head_dim: int, num_pages: int,
+                 page_tokens: int = 16, group: int = 128, sign_seed: int = 0,
+                 quant: int = KVC_QUANT_ASYM, signs: int = KVC_SIGNS_GLOBAL, pool=None,
+                 device="cuda"):
+        import torch
+        d = kvc_cache_desc(layers, kv_heads, head_dim, 4, group, quant, signs, 0,
+                           sign_seed & (2 ** 64 - 1), page_tokens, 0, num_pages)
+        block = kvc_cache_block_bytes(d)
+        if block == 0:
+            raise KvcError(KVC_ERR_INVALID_ARG, "kvc_cache_block_bytes")
+        if pool is None:
+            pool = torch.zeros(layers, num_pages, 2, kv_heads, block, dtype=torch.uint8,
+                               device=device)
+        if (tuple(pool.shape) != (layers, num_pages, 2, kv_heads, block) or not pool.is_cuda or
+                pool.dtype != torch.uint8 or (pool.numel() and pool.stride(4) != 1)):
+            raise ValueError(f"pool: expects a CUDA uint8 tensor {(layers, num_pages, 2, kv_heads, block)}")
+        self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
+        self._ws = {}
+        self._set(d, pool)
+
+    def _set(self, d, pool):
+        d.layers = pool.shape[0]
+        d.pool = pool.data_ptr() if pool.numel() else None
+        d.stride_layer, d.stride_page, d.stride_kv, d.stride_head = _strides(pool)
+        self.desc, self.pool, self.device = d, pool, pool.device
+
+    def __getitem__(self, which) -> "PagedCache":
+        if isinstance(which, int):
+            which = slice(which, which + 1 or None)
+        first, _, step = which.indices(self.pool.shape[0])
+        if step != 1:
+            raise ValueError("layers are taken in order")
+        view = object.__new__(PagedCache)
+        view.status, view._ws = self.status, self._ws
+        d = kvc_cache_desc()
+        C.pointer(d)[0] = self.desc
+        d.first_layer += first
+        view._set(d, self.pool[which])
+        return view
+
+    def _here(self, stream, **tensors):
+        """The stream, after a look at where the tensors are."""
+        import torch
+        if torch.cuda.current_device() != self.device.index:
+            raise ValueError(f"the cache is on {self.device}, which is not the current device")
+        for name, t in tensors.items():
+            if t is not None and t.device != self.device:
+                raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
+        return torch.cuda.current_stream(self.device) if stream is None else stream
+
+    def _workspace(self, stream, nbytes: int):
+        import torch
+        if torch.cuda.is_current_stream_capturing():  # a graph's own, from its memory pool
+            return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        ws = self._ws.get(stream.cuda_stream)
+        if ws is None or ws.numel() < nbytes:
+            if ws is not None:
+                ws.record_stream(stream)
+            with torch.cuda.stream(stream):
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            self._ws[stream.cuda_stream] = ws
+        return ws
+
+    @staticmethod
+    def _dtype(name, t):
+        import torch
+        if t.dtype == torch.bfloat16:
+            return KVC_BF16
+        if t.dtype == torch.float16:
+            return KVC_FP16
+        raise KvcError(KVC_ERR_UNSUPPORTED, f"{name}: {t.dtype}")
+
+    def _rows(self, k, v, slots):
+        import torch
+        d = self.desc
+        if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
+            raise ValueError("slots: expects a contiguous int64 vector")
+        shape = (d.layers, slots.numel(), d.kv_heads, d.head_dim)
+        for name, t in (("k", k), ("v", v)):
+            if tuple(t.shape) != shape or t.dtype != k.dtype or (t.numel() and t.stride(3) != 1):
+                raise ValueError(f"{name}: expects {shape} of one type, head_dim contiguous; got "
+                                 f"{tuple(t.shape)} {t.dtype}")
+        return kvc_cache_rows(self._dtype("k", k), 0, slots.numel(), k.data_ptr(), v.data_ptr(),
+                              *_strides(k), *_strides(v), slots.data_ptr())
+
+    def write(self, k, v, slots, stream=None):
+        """Quantises tokens' k and v ([layers, tokens, kv_heads, head_dim], bf16 or
+        fp16, any strides that are multiples of 8) into ``slots`` (device int64;
+        negative: skipped)."""
+        s = self._here(stream, k=k, v=v, slots=slots)
+        _check(kvc_cache_write(self.desc, self._rows(k, v, slots), self.status.data_ptr(),
+                               C.c_void_p(s.cuda_stream)), "kvc_cache_write")
+
+    def read(self, slots, k=None, v=None, dtype=None, stream=None):
+        """The rows stored in ``slots``, into k and v (made here if not given, with
+        zeros for negative slots; rows of given tensors are left as they were)."""
+        import torch
+        if (k is None) != (v is None):
+            raise ValueError("give both k and v, or neither")
+        s = self._here(stream, k=k, v=v, slots=slots)
+        if k is None:
+            d = self.desc
+            with torch.cuda.stream(s):
+                k, v = (torch.zeros(d.layers, slots.numel(), d.kv_heads, d.head_dim,
+                                    dtype=dtype or torch.bfloat16, device=self.device)
+                        for _ in range(2))
+        _check(kvc_cache_read(self.desc, self._rows(k, v, slots), self.status.data_ptr(),
+                              C.c_void_p(s.cuda_stream)), "kvc_cache_read")
+        return k, v
+
+    def load(self, stream_buf, nbytes: int, slots, seq_lens, stream=None, check: bool = False):
+        """Puts a compressed stream's codes into ``slots`` (one per token, requests in
+        order). Its own status word is read with check=True (which waits); else it
+        goes unread, and a bad stream shows only in ``load``'s workspace."""
+        import torch
+        if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
+            raise ValueError("slots: expects a contiguous int64 vector")
+        if slots.numel() != sum(seq_lens):
+            raise ValueError(f"{slots.numel()} slots for {sum(seq_lens)} tokens")
+        if stream_buf.dtype != torch.uint8 or stream_buf.numel() < int(nbytes) or \
+                not stream_buf.is_contiguous():
+            raise ValueError("stream_buf: expects a contiguous uint8 buffer of nbytes")
+        s = self._here(stream, stream_buf=stream_buf, slots=slots)
+        seq = [int(x) for x in seq_lens]
+        need = kvc_cache_load_workspace_bytes(self.desc, seq)
+        if need == 0:
+            raise KvcError(KVC_ERR_INVALID_ARG, "kvc_cache_load_workspace_bytes")
+        ws = self._workspace(s, need)
+        sp = C.c_void_p(s.cuda_stream)
+        _check(kvc_cache_load(stream_buf.data_ptr(), int(nbytes), self.desc, seq, slots.data_ptr(),
+                              ws.data_ptr(), ws.numel(), sp), "kvc_cache_load")
+        if check:
+            _check(kvc_stream_status(ws.data_ptr(), sp), "kvc_cache_load (device)")
+
+    def attend(self, q, page_table, seq_lens, q_starts=None, max_q: int = 1, out=None, lse=None,
+               scale: float | None = None, causal: bool = True, window: int = 0, stream=None):
+        """Attention of q ([layers, rows, heads, head_dim], bf16 or fp16) over the
+        requests' pages: page_table int32 [n_requests, pages], seq_lens int32
+        [n_requests] (the query tokens' own keys among them), q_starts int32
+        [n_requests + 1] (none: row r is request r's one query), all on the device;
+        max_q: the most queries of one request. Returns out (made here with zeros
+        if not given); lse, if given, is fp32 [layers, rows, heads]."""
+        import torch
+        d = self.desc
+        s = self._here(stream, q=q, page_table=page_table, seq_lens=seq_lens, q_starts=q_starts,
+                       out=out, lse=lse)
+        n = seq_lens.numel()
+        if q.dim() != 4 or q.shape[0] != d.layers or q.shape[3] != d.head_dim or \
+                q.shape[2] % max(d.kv_heads, 1) or (q.numel() and q.stride(3) != 1):
+            raise ValueError(f"q: expects [{d.layers}, rows, a multiple of {d.kv_heads}, {d.head_dim}]")
+        for name, t, shape in (("page_table", page_table, (n, page_table.shape[-1])),
+                               ("seq_lens", seq_lens, (n,)), ("q_starts", q_starts, (n + 1,))):
+            if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != shape or
+                                  (t.numel() and t.stride(-1) != 1)):
+                raise ValueError(f"{name}: expects int32 {shape}")
+        if out is None:
+            with torch.cuda.stream(s):
+                out = torch.zeros(q.shape, dtype=q.dtype, device=self.device)
+        if out.shape != q.shape or out.dtype != q.dtype or (out.numel() and out.stride(3) != 1):
+            raise ValueError("out: expects the shape and type of q")
+        if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:3] or
+                                not lse.is_contiguous()):
+            raise ValueError("lse: expects contiguous float32 [layers, rows, heads]")
+        t = kvc_cache_attn(self._dtype("q", q), q.shape[2] // max(d.kv_heads, 1), n, max_q,
+                           1 if causal else 0, window,
+                           d.head_dim ** -0.5 if scale is None else scale, 0, q.shape[1],
+                           None if q_starts is None else q_starts.data_ptr(), seq_lens.data_ptr(),
+                           page_table.data_ptr(), page_table.stride(0) if n > 1 else page_table.shape[1],
+                           q.data_ptr(), *_strides(q), out.data_ptr(), *_strides(out),
+                           None if lse is None else lse.data_ptr())
+        need = kvc_cache_attend_workspace_bytes(d, t)
+        ws = self._workspace(s, max(need, 1))
+        _check(kvc_cache_attend(d, t, ws.data_ptr(), ws.numel(), self.status.data_ptr(),
+                                C.c_void_p(s.cuda_stream)), "kvc_cache_attend")
+        return out
+
+    def check(self, stream=None):
+        """Waits for the stream, raises the first data-dependent error since the last
+        check, and clears it."""
+        s = self._here(stream)
+        sp = C.c_void_p(s.cuda_stream)
+        st = kvc_stream_status(self.status.data_ptr(), sp)
+        if st != KVC_OK:
+            kvc_cache_status_clear(self.status.data_ptr(), sp)
+            raise KvcError(st, "PagedCache (device)")

@@ -1,0 +1,90 @@
+// Shared by the host side and the kernels of the paged 4-bit cache
+// (kvc_cache_* in include/kvc.h).
+#pragma once
+
+#include "kvc_internal.h"
+
+namespace kvc {
+
+constexpr int kTileTok = 16;  // tokens per tile of a block
+
+KVC_HD constexpr uint32_t cache_code_bytes(int d) { return uint32_t(d) / 2; }
+KVC_HD constexpr uint32_t cache_tile_bytes(int d, int g) {
+  return kTileTok * (cache_code_bytes(d) + uint32_t(d / g) * 4);
+}
+
+// The pool as the kernels see it. `seed` is the state whose diagonal 0 is that
+// of (layer 0 of the description, keys, head 0); w0 and w1 are the global
+// diagonal's sign words.
+struct CachePool {
+  uint8_t *pool;
+  int64_t s_l, s_p, s_kv, s_h;  // bytes
+  uint32_t layers, heads;
+  uint32_t slots;     // num_pages * page_tokens (below 2^32)
+  uint32_t num_pages;
+  FastDiv pt;         // page_tokens
+  uint32_t vec_signs, sym;
+  uint64_t seed, w0, w1;
+};
+
+// New or stored rows (kvc_cache_rows), strides in bytes.
+struct RowArgs {
+  uint8_t *k, *v;
+  int64_t k_l, k_t, k_h, v_l, v_t, v_h;
+  uint32_t tokens;
+  const int64_t *slots;
+  uint32_t *status;  // may be null
+  float one;         // 1.0: the quantiser's integer rounding multiplies by it
+};
+
+// kvc_cache_load: the stream, checked against the pool's description.
+struct LoadArgs {
+  DecArgs d;  // header fields, status and the expanded meta chunks
+  uint32_t group;
+  const int64_t *slots;
+};
+
+// kvc_cache_attend. Strides in bytes.
+struct CacheAttnArgs {
+  CachePool c;
+  uint32_t n_req, qpk, max_q, causal, window;
+  float scale;              // the call's scale x log2(e) / head_dim
+  uint32_t q_tokens;
+  const int32_t *q_starts;  // null: one query per request
+  const int32_t *seq_lens;
+  const int32_t *page_table;
+  int64_t pt_stride;
+  uint32_t max_len;         // tokens a row of the page table can name
+  uint32_t max_blocks;      // blocks of query rows of all requests, at most
+  FastDiv tpp;              // tiles per page
+  const uint8_t *q;
+  int64_t q_l, q_t, q_h;
+  uint8_t *out;
+  int64_t o_l, o_t, o_h;
+  float *lse;
+  uint32_t *status;
+  // workspace: per request prefixes (work, column tiles), then the records
+  uint64_t *wpre;
+  uint32_t *cpre;
+  float *rec;
+};
+
+// Columns (query rows) of one unit of the attention: max_q * q_per_kv rounded
+// up to 4, 8 or 16; more come in several units of 16.
+inline int cache_cols(uint64_t rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
+// CTAs of an attention launch at most (the workspace holds a record for each
+// beside one per unit): 4 for each of 160 SMs.
+constexpr uint32_t kCacheGridMax = 640;
+
+cudaError_t launch_cache_write(int d, int g, int dtype, const CachePool &c, const RowArgs &r,
+                               int sms, cudaStream_t st);
+cudaError_t launch_cache_read(int d, int g, int dtype, const CachePool &c, const RowArgs &r,
+                              int sms, cudaStream_t st);
+cudaError_t launch_cache_load(int d, int g, const CachePool &c, const LoadArgs &l, int sms,
+                              cudaStream_t st);
+cudaError_t launch_cache_attend_d128(int g, int dtype, const CacheAttnArgs &a, int sms,
+                                     cudaStream_t st);
+cudaError_t launch_cache_attend_d64(int g, int dtype, const CacheAttnArgs &a, int sms,
+                                    cudaStream_t st);
+
+}  // namespace kvc

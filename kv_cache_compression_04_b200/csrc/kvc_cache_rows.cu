@@ -1,0 +1,499 @@
+// Writing, reading and loading rows of the paged 4-bit cache.
+//
+// A vector is held by four lanes: lane p of the four has channels 32*b + 8*p
+// .. + 7 of every 32-channel block b, i.e. one 4-byte code word per block. So
+// a 32-lane load takes 64 contiguous bytes of each of eight rows, the
+// butterfly's strides 1, 2, 4 and 32, 64 stay in registers and only 8 and 16
+// cross lanes (two shuffles per channel), and the stored orders (a key's words
+// and a value's halfwords transposed, include/kvc.h) are what a lane holds:
+// its words are 4 * (head_dim / 32) consecutive bytes of a key row, their
+// halves two consecutive runs of a value row.
+#include "kvc_cache.h"
+#include "kvc_launch.cuh"
+
+namespace kvc {
+
+namespace {
+
+constexpr int kRowWarps = 4;
+constexpr int kRowThreads = kRowWarps * 32;
+constexpr int kRowTok = kRowWarps * 8;  // tokens per CTA
+
+__device__ __forceinline__ void note(uint32_t *status, uint32_t code) {
+  if (status) set_status(status, code);
+}
+
+// The row of a slot in (layer, kv, head)'s blocks: its codes, and its meta.
+template <int D, int G>
+struct Place {
+  uint8_t *codes, *meta;
+  __device__ __forceinline__ Place(const CachePool &c, uint32_t slot, uint32_t l, uint32_t kv,
+                                   uint32_t h) {
+    const uint32_t page = fdiv(c.pt, slot), in = slot - page * c.pt.d;
+    const uint32_t tile = in / kTileTok, lane = in % kTileTok;
+    uint8_t *t = c.pool + int64_t(l) * c.s_l + int64_t(page) * c.s_p + int64_t(kv) * c.s_kv +
+                 int64_t(h) * c.s_h + uint64_t(tile) * cache_tile_bytes(D, G);
+    codes = t + lane * cache_code_bytes(D);
+    meta = t + kTileTok * cache_code_bytes(D) + lane * (D / G * 4);
+  }
+};
+
+// Sign bits of the lane's eight channels of every block: bit i of byte b.
+template <int D>
+__device__ __forceinline__ uint32_t lane_signs(const CachePool &c, uint32_t lkh, uint32_t p) {
+  uint64_t w0 = c.w0, w1 = c.w1;
+  if (c.vec_signs) {
+    uint64_t st = c.seed + uint64_t(lkh) * uint64_t(D / 64) * 0x9E3779B97F4A7C15ull;
+    w0 = splitmix64(st);
+    if constexpr (D == 128) w1 = splitmix64(st);
+  }
+  uint32_t s = uint32_t(w0 >> (8 * p)) & 0xFFu;
+  s |= (uint32_t(w0 >> (32 + 8 * p)) & 0xFFu) << 8;
+  if constexpr (D == 128) {
+    s |= (uint32_t(w1 >> (8 * p)) & 0xFFu) << 16;
+    s |= (uint32_t(w1 >> (32 + 8 * p)) & 0xFFu) << 24;
+  }
+  return s;
+}
+
+// y[j][i]: channel i of blocks j and j + D / 64 (x, y). The butterfly of
+// reading R2 (strides ascending, one rounding each): 1, 2, 4 between i; 8 and
+// 16 between lanes (b - a as a fused a * -1 + b, the same rounding); 32 between
+// j (d = 128), d / 2 inside each pair.
+template <int D>
+__device__ __forceinline__ void fwht_lanes(float2 (&y)[D / 64][8], uint32_t p) {
+  constexpr int N = D / 64;
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if ((i & h) == 0) {
+          const float2 a = y[j][i], b = y[j][i + h];
+          y[j][i] = add2(a, b);
+          y[j][i + h] = sub2(a, b);
+        }
+#pragma unroll
+  for (uint32_t s = 1; s < 4; s <<= 1) {
+    const float sg = (p & s) ? -1.0f : 1.0f;
+    const float2 sg2 = make_float2(sg, sg);
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 o = make_float2(__shfl_xor_sync(0xFFFFFFFFu, y[j][i].x, s),
+                                     __shfl_xor_sync(0xFFFFFFFFu, y[j][i].y, s));
+        y[j][i] = fma2(y[j][i], sg2, o);
+      }
+  }
+  if constexpr (N == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 a = y[0][i], b = y[1][i];
+      y[0][i] = add2(a, b);
+      y[1][i] = sub2(a, b);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = y[j][i].x, b = y[j][i].y;
+      y[j][i] = make_float2(__fadd_rn(a, b), __fsub_rn(a, b));
+    }
+}
+
+// Eight 16-bit values and their sign bits -> fp32.
+template <int DT>
+__device__ __forceinline__ void widen8(const uint4 &v, uint32_t s, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t x = w[k] ^ (((s >> (2 * k)) & 1u) << 15) ^ (((s >> (2 * k + 1)) & 1u) << 31);
+    if constexpr (DT == KVC_BF16) {
+      f[2 * k] = __uint_as_float(x << 16);
+      f[2 * k + 1] = __uint_as_float(x & 0xFFFF0000u);
+    } else {
+      f[2 * k] = __half2float(__ushort_as_half(uint16_t(x)));
+      f[2 * k + 1] = __half2float(__ushort_as_half(uint16_t(x >> 16)));
+    }
+  }
+}
+
+// Minimum and maximum over the four lanes of a vector.
+__device__ __forceinline__ void lanes_minmax(float &mn, float &mx) {
+#pragma unroll
+  for (uint32_t s = 1; s < 4; s <<= 1) {
+    mn = min2n(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, s));
+    mx = max2n(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, s));
+  }
+}
+
+// Scale, zero and code rules of readings R5 and R19 (Enc::quantize), for one
+// group's minimum and maximum.
+struct Group {
+  float zf, r;    // subtracted before the product, reciprocal of the scale
+  uint32_t meta;  // fp16 scale, fp16 zero
+  uint32_t err;   // 1: not finite, 2: fp16 overflow
+};
+__device__ __forceinline__ Group group_of(float mn, float mx, uint32_t sym) {
+  constexpr float down = 0.125f, up = 8.0f;
+  Group g{};
+  mn = __fadd_rn(mn, 0.0f);
+  mx = __fadd_rn(mx, 0.0f);
+  __half zh, sh;
+  if (sym) {
+    const float am = max2n(fabsf(mn), fabsf(mx));
+    sh = __float2half_ru(__fmul_rn(div_const<7>(am), down));
+    zh = (__half_as_ushort(sh) & 0x7FFFu) == 0
+             ? __ushort_as_half(0)
+             : __float2half_rd(__fmul_rn(__half2float(sh), -8.0f));
+    g.zf = 0.0f;
+  } else {
+    zh = __float2half_rd(__fmul_rn(mn, down));
+    g.zf = __fmul_rn(__half2float(zh), up);
+    sh = __float2half_ru(__fmul_rn(div_const<15>(__fsub_rn(mx, g.zf)), down));
+  }
+  const float sf = __fmul_rn(__half2float(sh), up);
+  g.r = sf == 0.0f ? 0.0f : rcp_scale(sf);
+  g.meta = uint32_t(__half_as_ushort(sh)) | (uint32_t(__half_as_ushort(zh)) << 16);
+  if (!(isfinite(mn) && isfinite(mx)))
+    g.err = 1u;
+  else if (!(isfinite(__half2float(zh)) && isfinite(sf)))
+    g.err = 2u;
+  return g;
+}
+
+// The lane's words (one per block) to a stored row, or from it.
+template <int D>
+__device__ __forceinline__ void put_words(uint8_t *codes, uint32_t p, uint32_t kv,
+                                          const uint32_t (&w)[D / 32]) {
+  if constexpr (D == 128) {
+    uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+    if (kv)
+      v = make_uint4(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410),
+                     __byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x7632));
+    *reinterpret_cast<uint4 *>(codes + 16 * p) = v;
+  } else {
+    uint2 v = make_uint2(w[0], w[1]);
+    if (kv) v = make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632));
+    *reinterpret_cast<uint2 *>(codes + 8 * p) = v;
+  }
+}
+template <int D>
+__device__ __forceinline__ void get_words(const uint8_t *codes, uint32_t p, uint32_t kv,
+                                          uint32_t (&w)[D / 32]) {
+  if constexpr (D == 128) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(codes + 16 * p);
+    w[0] = kv ? __byte_perm(v.x, v.z, 0x5410) : v.x;
+    w[1] = kv ? __byte_perm(v.x, v.z, 0x7632) : v.y;
+    w[2] = kv ? __byte_perm(v.y, v.w, 0x5410) : v.z;
+    w[3] = kv ? __byte_perm(v.y, v.w, 0x7632) : v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2 *>(codes + 8 * p);
+    w[0] = kv ? __byte_perm(v.x, v.y, 0x5410) : v.x;
+    w[1] = kv ? __byte_perm(v.x, v.y, 0x7632) : v.y;
+  }
+}
+
+// The token's slot; none (0xFFFFFFFF, never a slot number) if it is skipped.
+__device__ __forceinline__ uint32_t slot_of(const RowArgs &r, const CachePool &c, uint32_t t) {
+  if (t >= r.tokens) return ~0u;
+  const int64_t s = __ldg(reinterpret_cast<const long long *>(r.slots) + t);
+  if (s < 0) return ~0u;
+  if (s >= int64_t(c.slots)) {
+    note(r.status, KVC_ERR_CORRUPT);
+    return ~0u;
+  }
+  return uint32_t(s);
+}
+
+template <int D, int G, int DT>
+__global__ void __launch_bounds__(kRowThreads)
+    cache_write_kernel(const __grid_constant__ CachePool c, const __grid_constant__ RowArgs r) {
+  constexpr int NB = D / 32, N = D / 64, NG = D / G;
+  const uint32_t lane = threadIdx.x & 31, p = lane & 3;
+  const uint32_t t = blockIdx.x * kRowTok + (threadIdx.x >> 5) * 8 + (lane >> 2);
+  const uint32_t slot = slot_of(r, c, t);
+  for (uint32_t lkh = blockIdx.y; lkh < c.layers * 2 * c.heads; lkh += gridDim.y) {
+    const uint32_t lk = lkh / c.heads, h = lkh - lk * c.heads, l = lk >> 1, kv = lk & 1;
+    const uint8_t *row = kv ? r.v + int64_t(l) * r.v_l + int64_t(t) * r.v_t + int64_t(h) * r.v_h
+                            : r.k + int64_t(l) * r.k_l + int64_t(t) * r.k_t + int64_t(h) * r.k_h;
+    uint4 in[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      in[b] = slot != ~0u ? __ldg(reinterpret_cast<const uint4 *>(row + 64 * b + 16 * p))
+                          : make_uint4(0, 0, 0, 0);
+    const uint32_t sg = lane_signs<D>(c, lkh, p);
+    float2 y[N][8];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      float a[8], b[8];
+      widen8<DT>(in[j], sg >> (8 * j), a);
+      widen8<DT>(in[j + N], sg >> (8 * (j + N)), b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[j][i] = make_float2(a[i], b[i]);
+    }
+    fwht_lanes<D>(y, p);
+    // minimum and maximum of every block, of every group, over the lanes
+    float mn[NB], mx[NB];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      mn[j] = mx[j] = y[j][0].x;
+      mn[j + N] = mx[j + N] = y[j][0].y;
+#pragma unroll
+      for (int i = 1; i < 8; ++i) {
+        mn[j] = min2n(mn[j], y[j][i].x);
+        mx[j] = max2n(mx[j], y[j][i].x);
+        mn[j + N] = min2n(mn[j + N], y[j][i].y);
+        mx[j + N] = max2n(mx[j + N], y[j][i].y);
+      }
+    }
+    Group g[NG];
+    uint32_t err = 0;
+#pragma unroll
+    for (int q = 0; q < NG; ++q) {
+      float lo = mn[q * (G / 32)], hi = mx[q * (G / 32)];
+#pragma unroll
+      for (int b = 1; b < G / 32; ++b) {
+        lo = min2n(lo, mn[q * (G / 32) + b]);
+        hi = max2n(hi, mx[q * (G / 32) + b]);
+      }
+      lanes_minmax(lo, hi);
+      g[q] = group_of(lo, hi, c.sym);
+      err |= g[q].err;
+    }
+    // codes: nearest integer (ties to even) of the fp32 product, see Enc::quantize
+    const float magic = c.sym ? 12582920.0f : 12582912.0f;
+    const float2 mag = make_float2(magic, magic), one2 = make_float2(r.one, r.one);
+    uint32_t w[NB];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int ga = j * 32 / G, gb = (j + N) * 32 / G;
+      uint32_t a = 0, b = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 d = sub2(y[j][i], make_float2(g[ga].zf, g[gb].zf));
+        const float2 q = fma2(mul2(d, make_float2(g[ga].r, g[gb].r)), one2, mag);
+        a |= (__float_as_uint(q.x) & 15u) << (4 * i);
+        b |= (__float_as_uint(q.y) & 15u) << (4 * i);
+      }
+      w[j] = a;
+      w[j + N] = b;
+    }
+    if (slot == ~0u) continue;
+    if (err) note(r.status, (err & 1u) ? KVC_ERR_NONFINITE : KVC_ERR_RANGE);
+    const Place<D, G> at(c, slot, l, kv, h);
+    put_words<D>(at.codes, p, kv, w);
+    // a vector with an error reads as NaN
+    if constexpr (NG == 1) {
+      if (p == 0) *reinterpret_cast<uint32_t *>(at.meta) = err ? 0x7FFF7FFFu : g[0].meta;
+    } else if constexpr (NG == 2) {
+      if (p < 2)
+        reinterpret_cast<uint32_t *>(at.meta)[p] = err ? 0x7FFF7FFFu : p ? g[1].meta : g[0].meta;
+    } else {
+      const uint32_t m = p & 2 ? (p & 1 ? g[3].meta : g[2].meta) : (p & 1 ? g[1].meta : g[0].meta);
+      reinterpret_cast<uint32_t *>(at.meta)[p] = err ? 0x7FFF7FFFu : m;
+    }
+  }
+}
+
+// y^ = zf + q * sf, the butterfly, x 2^-log2 d, signs, one rounding (reading R9;
+// zf and sf pre-scaled as in Dec::vector, which shows that this is exact).
+template <int D, int G, int DT>
+__global__ void __launch_bounds__(kRowThreads)
+    cache_read_kernel(const __grid_constant__ CachePool c, const __grid_constant__ RowArgs r) {
+  constexpr int NB = D / 32, N = D / 64;
+  const uint32_t lane = threadIdx.x & 31, p = lane & 3;
+  const uint32_t t = blockIdx.x * kRowTok + (threadIdx.x >> 5) * 8 + (lane >> 2);
+  const uint32_t slot = slot_of(r, c, t);
+  for (uint32_t lkh = blockIdx.y; lkh < c.layers * 2 * c.heads; lkh += gridDim.y) {
+    const uint32_t lk = lkh / c.heads, h = lkh - lk * c.heads, l = lk >> 1, kv = lk & 1;
+    const Place<D, G> at(c, slot != ~0u ? slot : 0, l, kv, h);
+    uint32_t w[NB], m[D / G];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) w[b] = 0;
+#pragma unroll
+    for (int q = 0; q < D / G; ++q) m[q] = 0;
+    if (slot != ~0u) {
+      get_words<D>(at.codes, p, kv, w);
+#pragma unroll
+      for (int q = 0; q < D / G; ++q) m[q] = reinterpret_cast<const uint32_t *>(at.meta)[q];
+    }
+    constexpr float up = 8.0f / float(D);
+    float2 y[N][8];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const uint32_t ma = m[j * 32 / G], mb = m[(j + N) * 32 / G];
+      const float2 sf = make_float2(__fmul_rn(__half2float(__ushort_as_half(uint16_t(ma))), up),
+                                    __fmul_rn(__half2float(__ushort_as_half(uint16_t(mb))), up));
+      const float2 zf =
+          make_float2(__fmul_rn(__half2float(__ushort_as_half(uint16_t(ma >> 16))), up),
+                      __fmul_rn(__half2float(__ushort_as_half(uint16_t(mb >> 16))), up));
+      const float2 mag = make_float2(12582912.0f, 12582912.0f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t a = ((w[j] >> (4 * i)) & 15u) | 0x4B400000u;
+        const uint32_t b = ((w[j + N] >> (4 * i)) & 15u) | 0x4B400000u;
+        const float2 q = sub2(make_float2(__uint_as_float(a), __uint_as_float(b)), mag);
+        y[j][i] = fma2(q, sf, zf);
+      }
+    }
+    fwht_lanes<D>(y, p);
+    if (slot == ~0u) continue;
+    const uint32_t sg = lane_signs<D>(c, lkh, p);
+    uint8_t *row = kv ? r.v + int64_t(l) * r.v_l + int64_t(t) * r.v_t + int64_t(h) * r.v_h
+                      : r.k + int64_t(l) * r.k_l + int64_t(t) * r.k_t + int64_t(h) * r.k_h;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 e = y[b % N][2 * k], f = y[b % N][2 * k + 1];
+        const float lo = b < N ? e.x : e.y, hi = b < N ? f.x : f.y;
+        if constexpr (DT == KVC_BF16) {
+          const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+          o[k] = *reinterpret_cast<const uint32_t *>(&x);
+        } else {
+          const __half2 x = __floats2half2_rn(lo, hi);
+          o[k] = *reinterpret_cast<const uint32_t *>(&x);
+        }
+        const uint32_t s = sg >> (8 * b + 2 * k);
+        o[k] ^= ((s & 1u) << 15) | ((s & 2u) << 30);
+      }
+      *reinterpret_cast<uint4 *>(row + 64 * b + 16 * p) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+}
+
+// Codes and meta of the stream's vectors to their tokens' slots. Every table
+// entry that a vector relies on is checked by the lanes that use it: its code
+// chunk raw and in place, its meta chunk raw inside the stream or eliminated
+// (then expanded, and checked, by meta_expand_kernel).
+template <int D, int G>
+__global__ void __launch_bounds__(kRowThreads)
+    cache_load_kernel(const __grid_constant__ CachePool c, const __grid_constant__ LoadArgs a) {
+  using C = Cfg<D, 4, G>;
+  __shared__ uint32_t ok_s;
+  __shared__ uint64_t base_s;
+  grid_dependency_wait();  // the meta expansion
+  const uint8_t *in = a.d.in, *table = in + kHeader;
+  if (threadIdx.x == 0) {
+    const StreamHdr h = parse_header<D>(a.d);
+    bool ok = h.ok && h.bits == 4 && h.group == a.group && h.quant <= 1 && !h.code_elim &&
+              h.vec_signs == c.vec_signs && h.seed == c.seed &&
+              h.data_base + uint64_t(a.d.V) * C::CB <= h.stream_bytes;
+    ok_s = ok;
+    base_s = h.data_base;
+    if (!ok) set_status(a.d.status, KVC_ERR_CORRUPT);
+  }
+  __syncthreads();
+  if (!ok_s) return;
+  const uint64_t base = base_s, code_bytes = uint64_t(a.d.V) * C::CB;
+  const uint64_t n_code = (code_bytes + kChunk - 1) / kChunk;
+  const uint32_t lane = threadIdx.x & 31, p = lane & 3;
+  const uint32_t T = uint32_t(a.d.tokens);
+  const uint32_t t = blockIdx.x * kRowTok + (threadIdx.x >> 5) * 8 + (lane >> 2);
+  if (t >= T) return;
+  const int64_t s64 = __ldg(reinterpret_cast<const long long *>(a.slots) + t);
+  if (s64 < 0) return;
+  if (s64 >= int64_t(c.slots)) {
+    set_status(a.d.status, KVC_ERR_CORRUPT);
+    return;
+  }
+  for (uint32_t lkh = blockIdx.y; lkh < c.layers * 2 * c.heads; lkh += gridDim.y) {
+    const uint32_t lk = lkh / c.heads, h = lkh - lk * c.heads, l = lk >> 1, kv = lk & 1;
+    const uint32_t v = lkh * T + t;
+    const uint64_t ck = uint64_t(v) * C::CB / kChunk;
+    const uint64_t e = ld_u64(table + 8 * ck), rest = code_bytes - ck * kChunk;
+    const uint32_t ms = v / C::VM, mlen = min(uint32_t(C::VM), a.d.V - ms * C::VM) * C::MB;
+    const uint64_t em = ld_u64(table + 8 * (n_code + ms));
+    const bool raw = entry_size(em) == mlen;
+    if (entry_size(e) != (rest < kChunk ? rest : uint64_t(kChunk)) || entry_pipe(e) != 0 ||
+        entry_offset(e) != ck * kChunk ||
+        (raw && (entry_pipe(em) != 0 || base + entry_offset(em) + mlen > ld_u64(in + 56)))) {
+      set_status(a.d.status, KVC_ERR_CORRUPT);
+      continue;
+    }
+    const uint32_t *src = reinterpret_cast<const uint32_t *>(in + base + uint64_t(v) * C::CB);
+    uint32_t w[D / 32];
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b) w[b] = __ldg(src + 4 * b + p);
+    const uint8_t *mp = (raw ? in + base + entry_offset(em) : a.d.ws_meta + uint64_t(ms) * kChunk) +
+                        uint64_t(v - ms * C::VM) * C::MB;
+    const Place<D, G> at(c, uint32_t(s64), l, kv, h);
+    put_words<D>(at.codes, p, kv, w);
+    if (p < uint32_t(C::NG))
+      reinterpret_cast<uint32_t *>(at.meta)[p] = reinterpret_cast<const uint32_t *>(mp)[p];
+  }
+}
+
+dim3 row_grid(const CachePool &c, uint32_t tokens) {
+  const uint32_t lkh = c.layers * 2 * c.heads;
+  return dim3((tokens + kRowTok - 1) / kRowTok, lkh < 65535u ? lkh : 65535u);
+}
+
+template <int D, int G>
+cudaError_t write_t(int dtype, const CachePool &c, const RowArgs &r, cudaStream_t st) {
+  if (dtype == KVC_BF16)
+    cache_write_kernel<D, G, KVC_BF16><<<row_grid(c, r.tokens), kRowThreads, 0, st>>>(c, r);
+  else
+    cache_write_kernel<D, G, KVC_FP16><<<row_grid(c, r.tokens), kRowThreads, 0, st>>>(c, r);
+  return cudaGetLastError();
+}
+template <int D, int G>
+cudaError_t read_t(int dtype, const CachePool &c, const RowArgs &r, cudaStream_t st) {
+  if (dtype == KVC_BF16)
+    cache_read_kernel<D, G, KVC_BF16><<<row_grid(c, r.tokens), kRowThreads, 0, st>>>(c, r);
+  else
+    cache_read_kernel<D, G, KVC_FP16><<<row_grid(c, r.tokens), kRowThreads, 0, st>>>(c, r);
+  return cudaGetLastError();
+}
+template <int D, int G>
+cudaError_t load_t(const CachePool &c, const LoadArgs &a, int sms, cudaStream_t st) {
+  // eliminated meta chunks into the workspace; after a memset, so in plain stream order
+  auto mk = meta_expand_kernel<D>;
+  struct MetaTag {};
+  cudaError_t e = prepare<MetaTag>(mk, meta_smem_bytes());
+  if (e != cudaSuccess) return e;
+  const uint32_t mcap = uint32_t(kMetaCtas) * uint32_t(sms);
+  const uint32_t n = a.d.ws_meta_chunks;
+  mk<<<n == 0 ? 1u : (n < mcap ? n : mcap), kMetaThreads, meta_smem_bytes(), st>>>(a.d);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = row_grid(c, a.d.V ? uint32_t(a.d.tokens) : 0u);
+  if (cfg.gridDim.x == 0) cfg.gridDim = dim3(1, 1);  // nothing to store: the header is checked
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_load_kernel<D, G>, c, a);
+}
+
+}  // namespace
+
+#define KVC_CACHE_DISPATCH(F, ...)                    \
+  (d == 128 ? (g == 128  ? F<128, 128>(__VA_ARGS__)   \
+               : g == 64 ? F<128, 64>(__VA_ARGS__)    \
+                         : F<128, 32>(__VA_ARGS__))   \
+            : (g == 64 ? F<64, 64>(__VA_ARGS__) : F<64, 32>(__VA_ARGS__)))
+
+cudaError_t launch_cache_write(int d, int g, int dtype, const CachePool &c, const RowArgs &r, int,
+                               cudaStream_t st) {
+  return KVC_CACHE_DISPATCH(write_t, dtype, c, r, st);
+}
+cudaError_t launch_cache_read(int d, int g, int dtype, const CachePool &c, const RowArgs &r, int,
+                              cudaStream_t st) {
+  return KVC_CACHE_DISPATCH(read_t, dtype, c, r, st);
+}
+cudaError_t launch_cache_load(int d, int g, const CachePool &c, const LoadArgs &a, int sms,
+                              cudaStream_t st) {
+  return KVC_CACHE_DISPATCH(load_t, c, a, sms, st);
+}
+
+}  // namespace kvc

@@ -63,18 +63,25 @@ struct CacheAttnArgs {
   int64_t o_l, o_t, o_h;
   float *lse;
   uint32_t *status;
-  // workspace: per request prefixes (work, column tiles), then the records
+  // workspace: per request prefixes of work and shapes (queries, first row, keys),
+  // query fragments per unit, records per unit and warp
   uint64_t *wpre;
-  uint32_t *cpre;
+  uint4 *shapes;
+  uint8_t *qws;
   float *rec;
 };
 
 // Columns (query rows) of one unit of the attention: max_q * q_per_kv rounded
 // up to 4, 8 or 16; more come in several units of 16.
 inline int cache_cols(uint64_t rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
-// CTAs of an attention launch at most (the workspace holds a record for each
-// beside one per unit): 4 for each of 160 SMs.
-constexpr uint32_t kCacheGridMax = 640;
+// A unit's query fragments in the workspace, bytes: 16-bit hi and lo parts, then
+// factors and sums.
+inline uint64_t cache_frag_bytes(int d, int cols) {
+  return uint64_t(cols == 4 ? 1 : cols / 8) * uint64_t(d / 16) * 32 * (cols == 4 ? 8 : 16) + 512;
+}
+// Warps of an attention launch at most (the workspace holds a record for each
+// beside one per unit): 16 for each of 160 SMs.
+constexpr uint32_t kCacheWarpsMax = 2560;
 
 cudaError_t launch_cache_write(int d, int g, int dtype, const CachePool &c, const RowArgs &r,
                                int sms, cudaStream_t st);

@@ -129,10 +129,10 @@ kvc_status load_shape(const kvc_cache_desc *c, const int32_t *seq_lens, int32_t 
   return KVC_OK;
 }
 
-// The attention's workspace: per request prefixes, then one record per unit
-// and per CTA (each cols x (4 + head_dim) fp32).
+// The attention's workspace: per request prefixes and shapes, query fragments per
+// unit, then one record per unit and per warp (each cols x (4 + head_dim) fp32).
 struct AttnWs {
-  uint64_t blocks = 0, cpre = 0, rec = 0, total = 0;
+  uint64_t blocks = 0, shapes = 0, frags = 0, rec = 0, total = 0;
 };
 kvc_status check_attn(const kvc_cache_desc *cache, const kvc_cache_attn *t, CachePool &p, AttnWs &w,
                       bool pool_too) {
@@ -151,10 +151,12 @@ kvc_status check_attn(const kvc_cache_desc *cache, const kvc_cache_attn *t, Cach
   const uint64_t rows = uint64_t(t->max_q) * qpk, cols = uint64_t(cache_cols(rows));
   w.blocks = uint64_t(t->q_tokens) * qpk / cols + uint64_t(t->n_requests);
   const uint64_t units = uint64_t(cache->layers) * heads * w.blocks;
-  if (units >= (uint64_t(1) << 31)) return KVC_ERR_UNSUPPORTED;
-  w.cpre = round256(8 * (uint64_t(t->n_requests) + 1));
-  w.rec = w.cpre + round256(4 * (uint64_t(t->n_requests) + 1));
-  w.total = w.rec + (units + kCacheGridMax) * cols * (4 + uint64_t(cache->head_dim)) * sizeof(float);
+  if (units >= (uint64_t(1) << 31) - 1) return KVC_ERR_UNSUPPORTED;
+  w.shapes = round256(8 * (uint64_t(t->n_requests) + 1));
+  w.frags = w.shapes + round256(16 * uint64_t(t->n_requests));
+  w.rec = round256(w.frags + units * cache_frag_bytes(cache->head_dim, int(cols)));
+  w.total =
+      w.rec + (units + kCacheWarpsMax) * cols * (4 + uint64_t(cache->head_dim)) * sizeof(float);
   return KVC_OK;
 }
 
@@ -305,7 +307,8 @@ kvc_status kvc_cache_attend(const kvc_cache_desc *cache, const kvc_cache_attn *t
   a.status = status;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   a.wpre = reinterpret_cast<uint64_t *>(ws);
-  a.cpre = reinterpret_cast<uint32_t *>(ws + w.cpre);
+  a.shapes = reinterpret_cast<uint4 *>(ws + w.shapes);
+  a.qws = ws + w.frags;
   a.rec = reinterpret_cast<float *>(ws + w.rec);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = cache->head_dim == 128

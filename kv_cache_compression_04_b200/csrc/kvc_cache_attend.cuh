@@ -56,7 +56,6 @@ namespace kvc {
 
 constexpr int kChunkTok = 2 * kTileTok;
 constexpr uint32_t kCaLead = 2;      // a segment's fixed work, in chunks
-constexpr uint32_t kCaMinShare = 3;  // chunks (and fixed work) per warp at least
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -89,6 +88,10 @@ __device__ __forceinline__ float half_lo(uint32_t m) {
 }
 __device__ __forceinline__ float half_hi(uint32_t m) {
   return __half2float(__ushort_as_half(uint16_t(m >> 16)));
+}
+// Whether a meta word's scale or zero is infinite or NaN.
+__device__ __forceinline__ bool not_finite(uint32_t m) {
+  return (m & 0x7C00u) == 0x7C00u || (m & 0x7C000000u) == 0x7C000000u;
 }
 // A meta word's z + 8 s.
 __device__ __forceinline__ float zero8(uint32_t m) { return fmaf(8.f, half_lo(m), half_hi(m)); }
@@ -154,8 +157,22 @@ __device__ __forceinline__ uint32_t unit_work(const ReqShape &s) {
 // Warp g (of all CTAs) takes the work [g * share, (g + 1) * share) of all units'
 // in a row.
 __device__ __forceinline__ uint64_t work_per_warp(uint64_t total, uint32_t warps) {
-  const uint64_t s = (total + warps - 1) / warps;
-  return s < kCaMinShare ? kCaMinShare : s;
+  return div64(total + warps - 1, warps);
+}
+// The largest r < n with in(r), for an in() that is true up to some r and false
+// after it (0 if it is false at once). The warp looks at 32 places at a time.
+template <class In>
+__device__ __forceinline__ uint32_t last_with(uint32_t n, In in) {
+  const uint32_t lane = threadIdx.x & 31;
+  uint32_t lo = 0, len = n;
+  while (len > 1) {
+    const uint32_t step = (len + 31) / 32, p = lane * step;
+    const uint32_t yes = __ballot_sync(0xFFFFFFFFu, p < len && in(lo + p));
+    const uint32_t k = yes ? 31 - __clz(yes) : 0;
+    lo += k * step;
+    len = min(step, len - k * step);
+  }
+  return lo;
 }
 
 template <int D, int G, int NB>
@@ -243,13 +260,10 @@ __global__ void __launch_bounds__(kCaPrepWarps * 32)
   const uint32_t unit = blockIdx.x - 1, lh = unit / a.max_blocks, block = unit - lh * a.max_blocks;
   const uint32_t l = lh / H, h = lh - l * H;
   // the request whose block this is: the last whose first block is not past it
-  uint32_t lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const uint32_t mid = (lo + hi + 1) >> 1;
-    const uint32_t q0 = a.q_starts ? uint32_t(max(0, __ldg(a.q_starts + mid))) : mid;
-    if (first_block<COLS>(a, q0, mid) <= block) lo = mid;
-    else hi = mid - 1;
-  }
+  const uint32_t lo = last_with(n, [&](uint32_t r) {
+    const uint32_t q0 = a.q_starts ? uint32_t(max(0, __ldg(a.q_starts + r))) : r;
+    return first_block<COLS>(a, q0, r) <= block;
+  });
   bool ok;
   const ReqShape rs = read_request(a, lo, ok);
   const uint32_t fb = first_block<COLS>(a, rs.q0, lo);
@@ -352,7 +366,7 @@ __global__ void __launch_bounds__(kCaPrepWarps * 32)
 struct Segment {
   uint32_t l, h, r, c0, nc;      // layer, kv head, request; the unit's query rows
   uint32_t first, chunks;        // the segment's chunks
-  uint64_t unit;
+  uint64_t unit, u0, u1;         // the unit, and its work [u0, u1)
   int32_t any_lo, any_hi, all_lo, all_hi;  // keys that some row sees, that every row sees
   ReqShape rs;
 };
@@ -366,12 +380,7 @@ __device__ __forceinline__ Segment segment_at(const CacheAttnArgs &a, const uint
   const uint64_t lh = div64(f, wpre[n]), in_lh = f - lh * wpre[n];
   s.l = uint32_t(lh) / a.c.heads;
   s.h = uint32_t(lh) - s.l * a.c.heads;
-  uint32_t lo = 0, hi = n - 1;  // largest r with wpre[r] <= in_lh
-  while (lo < hi) {
-    const uint32_t mid = (lo + hi + 1) >> 1;
-    if (wpre[mid] <= in_lh) lo = mid;
-    else hi = mid - 1;
-  }
+  const uint32_t lo = last_with(n, [&](uint32_t r) { return wpre[r] <= in_lh; });
   s.r = lo;
   s.rs = request_shape(a, lo);
   const uint32_t work = unit_work(s.rs);
@@ -385,6 +394,8 @@ __device__ __forceinline__ Segment segment_at(const CacheAttnArgs &a, const uint
   const uint32_t c_at = at > kCaLead ? at - kCaLead : 0, c_end = end > kCaLead ? end - kCaLead : 0;
   s.first = s.rs.chunk0 + c_at;
   s.chunks = c_end - c_at;
+  s.u0 = f - at;
+  s.u1 = s.u0 + work;
   f += end - at;
   // rows are ordered by query
   key_range(a, s.rs, s.c0 / a.qpk, s.any_lo, s.all_hi);
@@ -423,26 +434,18 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
   const uint32_t g = blockIdx.x * CW + warp;
   uint64_t f = uint64_t(g) * share;
   const uint64_t f_end = min(total, f + share);
-  // The CTA's whole share in one unit: its warps are merged to one record.
-  bool one_unit;
-  {
-    uint64_t f0 = uint64_t(blockIdx.x) * CW * share;
-    const uint64_t f1 = min(total, f0 + CW * share);
-    if (f0 >= f1) return;
-    const Segment s0 = segment_at<COLS>(a, wpre, f1, f0);
-    one_unit = f0 == f1 && s0.chunks != 0;
-  }
+  const uint64_t cta0 = uint64_t(blockIdx.x) * CW * share, cta1 = min(total, cta0 + CW * share);
+  if (cta0 >= cta1) return;
 
-  // a warp without chunks in a CTA of one unit still takes part in the merge
-  bool first_turn = one_unit;
-  while (f < f_end || first_turn) {
-    first_turn = false;
-    Segment s;
-    if (f < f_end) {
-      s = segment_at<COLS>(a, wpre, f_end, f);
-    } else {
-      s = Segment{};
-    }
+  do {
+    // a warp with nothing to do still looks whether it is to take part in a merge
+    const bool idle = f >= f_end;
+    uint64_t next = idle ? cta1 - 1 : f;
+    Segment s = segment_at<COLS>(a, wpre, idle ? cta1 : f_end, next);
+    if (idle) s.chunks = 0;
+    f = next;
+    // The CTA's whole share in one unit: its warps are merged to one record.
+    const bool one_unit = s.u0 <= cta0 && cta1 <= s.u1;
     if (s.chunks == 0 && !one_unit) continue;
 
     // ---- the segment's chunks, copied ahead of their use (the unit's fragments are
@@ -505,18 +508,19 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
     constexpr int R = C::RB * C::LR;
     auto row_of = [&](int i) { return NB == 1 ? tq : 8 * (i / 2) + 2 * tq + i % 2; };
     float m[R], thr[R], ls[R], z[R][NG], oacc[C::MT][C::RB][4];
-    float fc[R], qsum[R][NG];
+    // (four groups: their sums are read at each chunk, from L1)
+    const float *qx = reinterpret_cast<const float *>(qsrc + C::QF);
+    float fc[R], qsum[R][NG < 4 ? NG : 1];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       m[i] = 0.f;           // (0 while thr is -inf)
       thr[i] = -INFINITY;   // raw score past which m is raised
       ls[i] = 0.f;
-      const float *qx = reinterpret_cast<const float *>(qsrc + C::QF);
       fc[i] = mine ? __ldg(qx + row_of(i)) : 1.f;
 #pragma unroll
       for (int gg = 0; gg < NG; ++gg) {
         z[i][gg] = 0.f;
-        qsum[i][gg] = mine ? __ldg(qx + COLS + row_of(i) * NG + gg) : 0.f;
+        if constexpr (NG < 4) qsum[i][gg] = mine ? __ldg(qx + COLS + row_of(i) * NG + gg) : 0.f;
       }
     }
 #pragma unroll
@@ -596,8 +600,9 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
               for (int i = 0; i < R; ++i) {
                 const float cA = NB == 1 ? acc[x][0][0] + acc[x][0][1] : acc[x][i / 2][i % 2];
                 const float cB = NB == 1 ? acc[x][0][2] + acc[x][0][3] : acc[x][i / 2][2 + i % 2];
-                sc[x][i][0] = fmaf(sA, cA, fmaf(zA, qsum[i][gg], sc[x][i][0]));
-                sc[x][i][1] = fmaf(sB, cB, fmaf(zB, qsum[i][gg], sc[x][i][1]));
+                const float qg = NG < 4 ? qsum[i][NG < 4 ? gg : 0] : qx[COLS + row_of(i) * NG + gg];
+                sc[x][i][0] = fmaf(sA, cA, fmaf(zA, qg, sc[x][i][0]));
+                sc[x][i][1] = fmaf(sB, cB, fmaf(zB, qg, sc[x][i][1]));
               }
             }
           }
@@ -627,13 +632,24 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
               if (!there || a0 < lim[i].x || a0 >= lim[i].y) sc[x][i][0] = -INFINITY;
               if (!there || b0 < lim[i].x || b0 >= lim[i].y) sc[x][i][1] = -INFINITY;
             }
-            // slots that no row sees may hold anything
-            const bool inA = there && a0 >= s.any_lo && a0 < s.any_hi;
-            const bool inB = there && b0 >= s.any_lo && b0 < s.any_hi;
+            // A value whose scale or zero is not finite: the rows that see the key get
+            // NaN through its score, the others (and slots that no row sees, which may
+            // hold anything) weigh it 0.
+            bool odd_a = false, odd_b = false;
 #pragma unroll
             for (int gg = 0; gg < NG; ++gg) {
-              vA[x][gg] = inA ? vA[x][gg] : 0u;
-              vB[x][gg] = inB ? vB[x][gg] : 0u;
+              odd_a |= not_finite(vA[x][gg]);
+              odd_b |= not_finite(vB[x][gg]);
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+              if (odd_a && sc[x][i][0] != -INFINITY) sc[x][i][0] = __uint_as_float(0x7FFFFFFFu);
+              if (odd_b && sc[x][i][1] != -INFINITY) sc[x][i][1] = __uint_as_float(0x7FFFFFFFu);
+            }
+#pragma unroll
+            for (int gg = 0; gg < NG; ++gg) {
+              vA[x][gg] = odd_a ? 0u : vA[x][gg];
+              vB[x][gg] = odd_b ? 0u : vB[x][gg];
             }
           }
         }
@@ -711,14 +727,7 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
             for (int i = 0; i < R; ++i) {
               w[i][0] = p[i][0] * sA;
               w[i][1] = p[i][1] * sB;
-              if (all) {
-                z[i][gg] = fmaf(p[i][0], zA, fmaf(p[i][1], zB, z[i][gg]));
-              } else {  // a hidden key weighs nothing, whatever its slot holds
-                if (p[i][0] == 0.f) w[i][0] = 0.f;
-                else z[i][gg] = fmaf(p[i][0], zA, z[i][gg]);
-                if (p[i][1] == 0.f) w[i][1] = 0.f;
-                else z[i][gg] = fmaf(p[i][1], zB, z[i][gg]);
-              }
+              z[i][gg] = fmaf(p[i][0], zA, fmaf(p[i][1], zB, z[i][gg]));
             }
 #pragma unroll
             for (int b = 0; b < C::RB; ++b)
@@ -799,12 +808,10 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
       }
       continue;
     }
-    // the CTA's warps, in their order (its first one has the unit: it starts there)
+    // the CTA's warps, in their order
     float *part = reinterpret_cast<float *>(smem);
     float2 *ml = reinterpret_cast<float2 *>(smem + C::ml);
-    uint64_t f0 = uint64_t(blockIdx.x) * CW * share;
-    const Segment s0 = segment_at<COLS>(a, wpre, min(total, f0 + CW * share), f0);
-    float *rec = a.rec + (s0.unit + uint64_t(blockIdx.x) * CW) * uint64_t(COLS * (4 + D));
+    float *rec = a.rec + (s.unit + uint64_t(blockIdx.x) * CW) * uint64_t(COLS * (4 + D));
 #pragma unroll
     for (int i = 0; i < R; ++i)
       if (gq == 0)
@@ -822,7 +829,7 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
               out4(blk, i);
       }
       __syncthreads();
-      const uint32_t rows = s0.nc > uint32_t(c0) ? min(s0.nc - c0, uint32_t(C::MC)) : 0;
+      const uint32_t rows = s.nc > uint32_t(c0) ? min(s.nc - c0, uint32_t(C::MC)) : 0;
       for (uint32_t i = tid; i < rows * D; i += C::THREADS) {
         const uint32_t col = i / D, ch = i % D;
         float M = -INFINITY;
@@ -842,7 +849,18 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
       }
     }
     return;
+  } while (f < f_end);
+}
+
+// Brings sums (L, y) under maximum M to maximum top >= M.
+__device__ __forceinline__ void merge_scale(float &M, float &L, float top, float (&y)[4]) {
+  if (M != -INFINITY && M != top) {
+    const float k = ex2(M - top);
+    L *= k;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[c] *= k;
   }
+  M = top;
 }
 
 // A row's records in turn, or split between WPR warps (few units, many records
@@ -862,15 +880,7 @@ __global__ void __launch_bounds__(WPR == 1 ? 128 : WPR * 32)
   const uint32_t j = uint32_t(i - lt * Hq), l = uint32_t(div64(lt, a.q_tokens));
   const uint32_t tok = uint32_t(lt - uint64_t(l) * a.q_tokens);
   uint32_t r = tok;
-  if (a.q_starts) {  // largest r with q_starts[r] <= tok
-    uint32_t lo = 0, hi = n;
-    while (lo < hi) {
-      const uint32_t mid = (lo + hi + 1) >> 1;
-      if (__ldg(a.q_starts + mid) <= int32_t(tok)) lo = mid;
-      else hi = mid - 1;
-    }
-    r = lo;
-  }
+  if (a.q_starts) r = last_with(n + 1, [&](uint32_t x) { return __ldg(a.q_starts + x) <= int32_t(tok); });
   if (r >= n) return;
   const ReqShape rs = request_shape(a, r);
   if (tok < rs.q0 || tok - rs.q0 >= rs.nq) return;  // a row that no request names
@@ -899,20 +909,27 @@ __global__ void __launch_bounds__(WPR == 1 ? 128 : WPR * 32)
     };
     constexpr uint32_t kStep = COLS * (4 + D);
     const float *p0 = a.rec + unit * uint64_t(kStep) + (row - block * COLS) * (4 + D);
-    for (uint32_t k = lane; k < nrec; k += 32) M = fmaxf(M, p0[uint64_t(warp_at(k)) * kStep]);
+    // four records at a time: their loads first, then the running maximum and sums
+    for (uint32_t k0 = WPR == 1 ? 0 : 4 * warp; k0 < nrec; k0 += 4 * WPR) {
+      float2 v[4];
+      float o[4][W];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-#pragma unroll 4
-    for (uint32_t k = WPR == 1 ? 0 : warp; k < nrec; k += WPR) {
-      const float *p = p0 + uint64_t(warp_at(k)) * kStep;
-      const float2 v = *reinterpret_cast<const float2 *>(p);
-      const bool none = v.x == -INFINITY && v.y == 0.f;  // no key of this row in the segment
-      const float w = none ? 0.f : v.x == -INFINITY ? 1.f : ex2(v.x - M);
-      L = fmaf(w, v.y, L);
+      for (int e = 0; e < 4; ++e) {
+        const bool in = k0 + e < nrec;
+        const float *p = p0 + uint64_t(warp_at(in ? k0 + e : k0)) * kStep;
+        v[e] = in ? *reinterpret_cast<const float2 *>(p) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int c = 0; c < W; ++c) {
-        const float x = p[4 + lane + 32 * c];
-        y[c] = none ? y[c] : fmaf(w, x, y[c]);
+        for (int c = 0; c < W; ++c) o[e][c] = p[4 + lane + 32 * c];
+      }
+      const float top = fmaxf(M, fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x)));
+      merge_scale(M, L, top, y);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (v[e].x == -INFINITY && v[e].y == 0.f) continue;  // no key of this row in the segment
+        const float w = v[e].x == -INFINITY ? 1.f : ex2(v[e].x - top);
+        L = fmaf(w, v[e].y, L);
+#pragma unroll
+        for (int c = 0; c < W; ++c) y[c] = fmaf(w, o[e][c], y[c]);
       }
     }
   }
@@ -922,14 +939,19 @@ __global__ void __launch_bounds__(WPR == 1 ? 128 : WPR * 32)
     if (lane == 0) ml[warp] = make_float2(M, L);
     __syncthreads();
     if (warp) return;
+#pragma unroll
+    for (int w = 1; w < WPR; ++w) M = fmaxf(M, ml[w].x);
     L = 0.f;
 #pragma unroll
     for (int c = 0; c < W; ++c) y[c] = 0.f;
 #pragma unroll
     for (int w = 0; w < WPR; ++w) {
-      L += ml[w].y;
+      const float2 v = ml[w];
+      if (v.x == -INFINITY && v.y == 0.f) continue;
+      const float k = v.x == -INFINITY ? 1.f : ex2(v.x - M);
+      L = fmaf(k, v.y, L);
 #pragma unroll
-      for (int c = 0; c < W; ++c) y[c] += part[w][lane + 32 * c];
+      for (int c = 0; c < W; ++c) y[c] = fmaf(k, part[w][lane + 32 * c], y[c]);
     }
   }
   const bool empty = M == -INFINITY && L == 0.f;

@@ -435,7 +435,7 @@ class Codec:
 
 def _strides(t):
     """Strides of all dimensions but the last; those that are never stepped along, 0."""
-    return [st if n > 1 else 0 for n, st in zip(t.shape[:-1], t.stride())]
+    return [st if n > 1 else 0 for n, st in zip(t.shape, t.stride())][:-1]
 
 
 class PagedCache:
@@ -480,6 +480,7 @@ class PagedCache:
         d.pool = pool.data_ptr() if pool.numel() else None
         d.stride_layer, d.stride_page, d.stride_kv, d.stride_head = _strides(pool)
         self.desc, self.pool, self.device = d, pool, pool.device
+        self.index, self._desc, self._status = pool.get_device(), C.byref(d), self.status.data_ptr()
 
     def __getitem__(self, which) -> "PagedCache":
         if isinstance(which, int):
@@ -495,31 +496,28 @@ class PagedCache:
         view._set(d, self.pool[which])
         return view
 
-    def _here(self, stream, **tensors):
-        """The stream, after a look at where the tensors are."""
+    def _here(self, stream, *tensors):
+        """The stream's handle, after a look at where the tensors are."""
         import torch
-        if torch.cuda.current_device() != self.device.index:
+        if torch._C._cuda_getDevice() != self.index:
             raise ValueError(f"the cache is on {self.device}, which is not the current device")
-        for name, t in tensors.items():
-            if t is not None and t.device != self.device:
-                raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
-        return torch.cuda.current_stream(self.device) if stream is None else stream
+        for t in tensors:
+            if t is not None and t.get_device() != self.index:
+                raise ValueError(f"a tensor is on {t.device}, the cache on {self.device}")
+        return torch._C._cuda_getCurrentRawStream(self.index) if stream is None else stream.cuda_stream
 
-    def _workspace(self, stream, nbytes: int):
+    def _workspace(self, stream, handle: int, nbytes: int):
         import torch
         if torch.cuda.is_current_stream_capturing():  # a graph's own, from its memory pool
             return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        ws = self._ws.get(stream.cuda_stream)
+        ws = self._ws.get(handle)
         if ws is None or ws.numel() < nbytes:
-            if ws is not None:
-                ws.record_stream(stream)
-            with torch.cuda.stream(stream):
+            with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream):
                 ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-            self._ws[stream.cuda_stream] = ws
+            self._ws[handle] = ws
         return ws
 
-    @staticmethod
-    def _dtype(name, t):
+    def _dtype(self, name, t):
         import torch
         if t.dtype == torch.bfloat16:
             return KVC_BF16
@@ -529,24 +527,24 @@ class PagedCache:
 
     def _rows(self, k, v, slots):
         import torch
-        d = self.desc
         if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
             raise ValueError("slots: expects a contiguous int64 vector")
-        shape = (d.layers, slots.numel(), d.kv_heads, d.head_dim)
+        n = slots.numel()
+        shape = (self.desc.layers, n, self.desc.kv_heads, self.desc.head_dim)
         for name, t in (("k", k), ("v", v)):
-            if tuple(t.shape) != shape or t.dtype != k.dtype or (t.numel() and t.stride(3) != 1):
+            if t.shape != shape or t.dtype != k.dtype or (n and t.stride(3) != 1):
                 raise ValueError(f"{name}: expects {shape} of one type, head_dim contiguous; got "
                                  f"{tuple(t.shape)} {t.dtype}")
-        return kvc_cache_rows(self._dtype("k", k), 0, slots.numel(), k.data_ptr(), v.data_ptr(),
+        return kvc_cache_rows(self._dtype("k", k), 0, n, k.data_ptr(), v.data_ptr(),
                               *_strides(k), *_strides(v), slots.data_ptr())
 
     def write(self, k, v, slots, stream=None):
         """Quantises tokens' k and v ([layers, tokens, kv_heads, head_dim], bf16 or
         fp16, any strides that are multiples of 8) into ``slots`` (device int64;
         negative: skipped)."""
-        s = self._here(stream, k=k, v=v, slots=slots)
-        _check(kvc_cache_write(self.desc, self._rows(k, v, slots), self.status.data_ptr(),
-                               C.c_void_p(s.cuda_stream)), "kvc_cache_write")
+        s = self._here(stream, k, v, slots)
+        _check(lib().kvc_cache_write(self._desc, C.byref(self._rows(k, v, slots)), self._status, s),
+               "kvc_cache_write")
 
     def read(self, slots, k=None, v=None, dtype=None, stream=None):
         """The rows stored in ``slots``, into k and v (made here if not given, with
@@ -554,15 +552,15 @@ class PagedCache:
         import torch
         if (k is None) != (v is None):
             raise ValueError("give both k and v, or neither")
-        s = self._here(stream, k=k, v=v, slots=slots)
+        s = self._here(stream, k, v, slots)
         if k is None:
             d = self.desc
-            with torch.cuda.stream(s):
+            with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream):
                 k, v = (torch.zeros(d.layers, slots.numel(), d.kv_heads, d.head_dim,
                                     dtype=dtype or torch.bfloat16, device=self.device)
                         for _ in range(2))
-        _check(kvc_cache_read(self.desc, self._rows(k, v, slots), self.status.data_ptr(),
-                              C.c_void_p(s.cuda_stream)), "kvc_cache_read")
+        _check(lib().kvc_cache_read(self._desc, C.byref(self._rows(k, v, slots)), self._status, s),
+               "kvc_cache_read")
         return k, v
 
     def load(self, stream_buf, nbytes: int, slots, seq_lens, stream=None, check: bool = False):
@@ -577,17 +575,16 @@ class PagedCache:
         if stream_buf.dtype != torch.uint8 or stream_buf.numel() < int(nbytes) or \
                 not stream_buf.is_contiguous():
             raise ValueError("stream_buf: expects a contiguous uint8 buffer of nbytes")
-        s = self._here(stream, stream_buf=stream_buf, slots=slots)
+        s = self._here(stream, stream_buf, slots)
         seq = [int(x) for x in seq_lens]
         need = kvc_cache_load_workspace_bytes(self.desc, seq)
         if need == 0:
             raise KvcError(KVC_ERR_INVALID_ARG, "kvc_cache_load_workspace_bytes")
-        ws = self._workspace(s, need)
-        sp = C.c_void_p(s.cuda_stream)
+        ws = self._workspace(stream, s, need)
         _check(kvc_cache_load(stream_buf.data_ptr(), int(nbytes), self.desc, seq, slots.data_ptr(),
-                              ws.data_ptr(), ws.numel(), sp), "kvc_cache_load")
+                              ws.data_ptr(), ws.numel(), s), "kvc_cache_load")
         if check:
-            _check(kvc_stream_status(ws.data_ptr(), sp), "kvc_cache_load (device)")
+            _check(kvc_stream_status(ws.data_ptr(), s), "kvc_cache_load (device)")
 
     def attend(self, q, page_table, seq_lens, q_starts=None, max_q: int = 1, out=None, lse=None,
                scale: float | None = None, causal: bool = True, window: int = 0, stream=None):
@@ -599,44 +596,45 @@ class PagedCache:
         if not given); lse, if given, is fp32 [layers, rows, heads]."""
         import torch
         d = self.desc
-        s = self._here(stream, q=q, page_table=page_table, seq_lens=seq_lens, q_starts=q_starts,
-                       out=out, lse=lse)
-        n = seq_lens.numel()
-        if q.dim() != 4 or q.shape[0] != d.layers or q.shape[3] != d.head_dim or \
-                q.shape[2] % max(d.kv_heads, 1) or (q.numel() and q.stride(3) != 1):
+        s = self._here(stream, q, page_table, seq_lens, q_starts, out, lse)
+        n, shape, heads, int32 = seq_lens.numel(), q.shape, max(d.kv_heads, 1), torch.int32
+        if len(shape) != 4 or shape[0] != d.layers or shape[3] != d.head_dim or \
+                shape[2] % heads or (shape[1] and q.stride(3) != 1):
             raise ValueError(f"q: expects [{d.layers}, rows, a multiple of {d.kv_heads}, {d.head_dim}]")
-        for name, t, shape in (("page_table", page_table, (n, page_table.shape[-1])),
-                               ("seq_lens", seq_lens, (n,)), ("q_starts", q_starts, (n + 1,))):
-            if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != shape or
-                                  (t.numel() and t.stride(-1) != 1)):
-                raise ValueError(f"{name}: expects int32 {shape}")
+        if page_table.dtype != int32 or page_table.dim() != 2 or page_table.shape[0] != n or \
+                (page_table.numel() and page_table.stride(1) != 1):
+            raise ValueError(f"page_table: expects int32 [{n}, pages]")
+        if seq_lens.dtype != int32 or seq_lens.dim() != 1 or (n > 1 and seq_lens.stride(0) != 1):
+            raise ValueError("seq_lens: expects an int32 vector")
+        if q_starts is not None and (q_starts.dtype != int32 or q_starts.shape != (n + 1,) or
+                                     not q_starts.is_contiguous()):
+            raise ValueError(f"q_starts: expects int32 [{n + 1}]")
         if out is None:
-            with torch.cuda.stream(s):
-                out = torch.zeros(q.shape, dtype=q.dtype, device=self.device)
-        if out.shape != q.shape or out.dtype != q.dtype or (out.numel() and out.stride(3) != 1):
+            with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream):
+                out = torch.zeros(shape, dtype=q.dtype, device=self.device)
+        elif out.shape != shape or out.dtype != q.dtype or (shape[1] and out.stride(3) != 1):
             raise ValueError("out: expects the shape and type of q")
-        if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:3] or
+        if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:3] or
                                 not lse.is_contiguous()):
             raise ValueError("lse: expects contiguous float32 [layers, rows, heads]")
-        t = kvc_cache_attn(self._dtype("q", q), q.shape[2] // max(d.kv_heads, 1), n, max_q,
-                           1 if causal else 0, window,
-                           d.head_dim ** -0.5 if scale is None else scale, 0, q.shape[1],
+        t = kvc_cache_attn(self._dtype("q", q), shape[2] // heads, n, max_q, 1 if causal else 0,
+                           window, d.head_dim ** -0.5 if scale is None else scale, 0, shape[1],
                            None if q_starts is None else q_starts.data_ptr(), seq_lens.data_ptr(),
-                           page_table.data_ptr(), page_table.stride(0) if n > 1 else page_table.shape[1],
+                           page_table.data_ptr(),
+                           page_table.stride(0) if n > 1 else page_table.shape[1],
                            q.data_ptr(), *_strides(q), out.data_ptr(), *_strides(out),
                            None if lse is None else lse.data_ptr())
-        need = kvc_cache_attend_workspace_bytes(d, t)
-        ws = self._workspace(s, max(need, 1))
-        _check(kvc_cache_attend(d, t, ws.data_ptr(), ws.numel(), self.status.data_ptr(),
-                                C.c_void_p(s.cuda_stream)), "kvc_cache_attend")
+        call, tp = lib(), C.byref(t)
+        ws = self._workspace(stream, s, max(call.kvc_cache_attend_workspace_bytes(self._desc, tp), 1))
+        _check(call.kvc_cache_attend(self._desc, tp, ws.data_ptr(), ws.numel(), self._status, s),
+               "kvc_cache_attend")
         return out
 
     def check(self, stream=None):
         """Waits for the stream, raises the first data-dependent error since the last
         check, and clears it."""
         s = self._here(stream)
-        sp = C.c_void_p(s.cuda_stream)
-        st = kvc_stream_status(self.status.data_ptr(), sp)
+        st = kvc_stream_status(self._status, s)
         if st != KVC_OK:
-            kvc_cache_status_clear(self.status.data_ptr(), sp)
+            kvc_cache_status_clear(self._status, s)
             raise KvcError(st, "PagedCache (device)")

@@ -184,9 +184,9 @@ struct CaCfg {
   static constexpr int RB = NB == 1 ? 1 : NB / 2;   // column blocks of either product
   static constexpr int LR = NB == 1 ? 1 : 2;        // rows a lane has per block
   static constexpr int KB = D / 16;                 // 16-channel steps of the score product
-  // Warps and CTAs per SM: 16 warps with 128 registers, 12 with 168 where a lane's
-  // state is that of 16 rows.
-  static constexpr int CW = NB <= 2 ? 8 : 12;
+  // Warps and CTAs per SM: 12 warps with 168 registers (16 with 128 spilled, and
+  // took as long or longer); as one CTA where it merges 16 rows.
+  static constexpr int CW = NB <= 2 ? 6 : 12;
   static constexpr int CTAS = NB <= 2 ? 2 : 1;
   static constexpr int THREADS = CW * 32;
   static constexpr uint32_t TB = cache_tile_bytes(D, G), CB = cache_code_bytes(D);

@@ -87,6 +87,16 @@ cudaError_t launch_cache_write(int d, int g, int dtype, const CachePool &c, cons
                                int sms, cudaStream_t st);
 cudaError_t launch_cache_read(int d, int g, int dtype, const CachePool &c, const RowArgs &r,
                               int sms, cudaStream_t st);
+// Many rows: blocks of 32 tokens of one (layer, kv, head) each.
+#define KVC_DECLARE_BLOCKS(K, D)                                                        \
+  cudaError_t launch_cache_##K##_blocks_d##D(int g, int dtype, const CachePool &c,      \
+                                             const RowArgs &r, uint32_t blocks, int sms, \
+                                             cudaStream_t st);
+KVC_DECLARE_BLOCKS(write, 128)
+KVC_DECLARE_BLOCKS(write, 64)
+KVC_DECLARE_BLOCKS(read, 128)
+KVC_DECLARE_BLOCKS(read, 64)
+#undef KVC_DECLARE_BLOCKS
 cudaError_t launch_cache_load(int d, int g, const CachePool &c, const LoadArgs &l, int sms,
                               cudaStream_t st);
 cudaError_t launch_cache_attend_d128(int g, int dtype, const CacheAttnArgs &a, int sms,

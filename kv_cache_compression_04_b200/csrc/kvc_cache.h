@@ -55,7 +55,7 @@ struct CacheAttnArgs {
   const int32_t *page_table;
   int64_t pt_stride;
   uint32_t max_len;         // tokens a row of the page table can name
-  uint32_t max_blocks;      // blocks of query rows of all requests, at most
+  uint32_t max_blocks;      // blocks of 128 query rows of all requests, at most
   FastDiv tpp;              // tiles per page
   const uint8_t *q;
   int64_t q_l, q_t, q_h;
@@ -65,23 +65,27 @@ struct CacheAttnArgs {
   uint32_t *status;
   // workspace: per request prefixes of work and shapes (queries, first row, keys),
   // query fragments per unit, records per unit and warp
-  uint64_t *wpre;
+  uint64_t *wpre;  // per request, or per block of 128 rows
   uint4 *shapes;
+  uint4 *blk;      // blocks of 128 rows: request, first row, first key tile, tiles
   uint8_t *qws;
   float *rec;
 };
 
-// Columns (query rows) of one unit of the attention: max_q * q_per_kv rounded
-// up to 4, 8 or 16; more come in several units of 16.
-inline int cache_cols(uint64_t rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
+// Query rows of one unit of the attention: a request's (queries x query heads per kv
+// head) rounded up to 4, 8 or 16, or blocks of 128 of more than 16.
+inline int cache_cols(uint64_t rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 128; }
 // A unit's query fragments in the workspace, bytes: 16-bit hi and lo parts, then
 // factors and sums.
 inline uint64_t cache_frag_bytes(int d, int cols) {
+  if (cols > 16) return 0;
   return uint64_t(cols == 4 ? 1 : cols / 8) * uint64_t(d / 16) * 32 * (cols == 4 ? 8 : 16) + 512;
 }
 // Warps of an attention launch at most (the workspace holds a record for each
 // beside one per unit): 16 for each of 160 SMs.
 constexpr uint32_t kCacheWarpsMax = 2560;
+// CTAs of a launch for blocks of 128 rows at most: one for each of 160 SMs.
+constexpr uint32_t kCachePrefillCtas = 160;
 
 cudaError_t launch_cache_write(int d, int g, int dtype, const CachePool &c, const RowArgs &r,
                                int sms, cudaStream_t st);
@@ -100,6 +104,10 @@ KVC_DECLARE_BLOCKS(read, 64)
 cudaError_t launch_cache_load(int d, int g, const CachePool &c, const LoadArgs &l, int sms,
                               cudaStream_t st);
 cudaError_t launch_cache_attend_d128(int g, int dtype, const CacheAttnArgs &a, int sms,
+                                     cudaStream_t st);
+cudaError_t launch_cache_prefill_d128(int g, int dtype, const CacheAttnArgs &a, int sms,
+                                      cudaStream_t st);
+cudaError_t launch_cache_prefill_d64(int g, int dtype, const CacheAttnArgs &a, int sms,
                                      cudaStream_t st);
 cudaError_t launch_cache_attend_d64(int g, int dtype, const CacheAttnArgs &a, int sms,
                                     cudaStream_t st);

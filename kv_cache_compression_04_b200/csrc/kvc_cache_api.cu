@@ -129,8 +129,10 @@ kvc_status load_shape(const kvc_cache_desc *c, const int32_t *seq_lens, int32_t 
   return KVC_OK;
 }
 
-// The attention's workspace: per request prefixes and shapes, query fragments per
-// unit, then one record per unit and per warp (each cols x (4 + head_dim) fp32).
+// The attention's workspace: prefixes of work and the requests' shapes; up to 16 rows per
+// request, query fragments per unit (layer, kv head, request); more, the blocks of 128
+// rows; then one record per unit (a block's, with more than 16 rows) and per warp or CTA
+// (each cols x (4 + head_dim) fp32).
 struct AttnWs {
   uint64_t blocks = 0, shapes = 0, frags = 0, rec = 0, total = 0;
 };
@@ -149,14 +151,18 @@ kvc_status check_attn(const kvc_cache_desc *cache, const kvc_cache_attn *t, Cach
   if (!t->q_starts && t->q_tokens < t->n_requests) return KVC_ERR_INVALID_ARG;
   const uint64_t heads = uint64_t(cache->kv_heads), qpk = uint64_t(t->q_per_kv);
   const uint64_t rows = uint64_t(t->max_q) * qpk, cols = uint64_t(cache_cols(rows));
-  w.blocks = uint64_t(t->q_tokens) * qpk / cols + uint64_t(t->n_requests);
-  const uint64_t units = uint64_t(cache->layers) * heads * w.blocks;
-  if (units >= (uint64_t(1) << 31) - 1) return KVC_ERR_UNSUPPORTED;
-  w.shapes = round256(8 * (uint64_t(t->n_requests) + 1));
-  w.frags = w.shapes + round256(16 * uint64_t(t->n_requests));
-  w.rec = round256(w.frags + units * cache_frag_bytes(cache->head_dim, int(cols)));
-  w.total =
-      w.rec + (units + kCacheWarpsMax) * cols * (4 + uint64_t(cache->head_dim)) * sizeof(float);
+  const uint64_t reqs = uint64_t(t->n_requests), lh = uint64_t(cache->layers) * heads;
+  w.blocks = cols > 16 ? uint64_t(t->q_tokens) * qpk / cols + reqs : reqs;
+  const uint64_t units = lh * w.blocks;
+  // (query rows of a request, and units, are counted in 32 bits)
+  if (units >= (uint64_t(1) << 31) - 1 || uint64_t(t->q_tokens) * qpk >= (uint64_t(1) << 31))
+    return KVC_ERR_UNSUPPORTED;
+  w.shapes = round256(8 * (w.blocks + 1));
+  w.frags = w.shapes + round256(16 * reqs);
+  const uint64_t frags = cols > 16 ? 16 * w.blocks : units * cache_frag_bytes(cache->head_dim, int(cols));
+  w.rec = round256(w.frags + frags);
+  w.total = w.rec + (units + (cols > 16 ? kCachePrefillCtas : kCacheWarpsMax)) * cols *
+                        (4 + uint64_t(cache->head_dim)) * sizeof(float);
   return KVC_OK;
 }
 
@@ -308,12 +314,18 @@ kvc_status kvc_cache_attend(const kvc_cache_desc *cache, const kvc_cache_attn *t
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   a.wpre = reinterpret_cast<uint64_t *>(ws);
   a.shapes = reinterpret_cast<uint4 *>(ws + w.shapes);
+  a.blk = reinterpret_cast<uint4 *>(ws + w.frags);
   a.qws = ws + w.frags;
   a.rec = reinterpret_cast<float *>(ws + w.rec);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = cache->head_dim == 128
-                            ? launch_cache_attend_d128(cache->group_size, t->dtype, a, sms, cs)
-                            : launch_cache_attend_d64(cache->group_size, t->dtype, a, sms, cs);
+  const int g = cache->group_size;
+  cudaError_t e;
+  if (uint64_t(t->max_q) * uint64_t(t->q_per_kv) > 16)
+    e = cache->head_dim == 128 ? launch_cache_prefill_d128(g, t->dtype, a, sms, cs)
+                               : launch_cache_prefill_d64(g, t->dtype, a, sms, cs);
+  else
+    e = cache->head_dim == 128 ? launch_cache_attend_d128(g, t->dtype, a, sms, cs)
+                               : launch_cache_attend_d64(g, t->dtype, a, sms, cs);
   return e == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 

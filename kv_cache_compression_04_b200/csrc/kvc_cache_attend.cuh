@@ -28,8 +28,11 @@
 // output to fp16). Up to 4 rows, columns 2 i, 2 i + 1 are row i's two parts in both
 // products.
 //
-// Work. A unit is (layer, kv head, request, block of query rows); its keys are
-// chunks of 32 tokens (two tiles). All units' chunks in a row, each unit with
+// Up to 16 query rows (queries x query heads per kv head) of a request; more are
+// kvc_cache_prefill.cuh's.
+//
+// Work. A unit is (layer, kv head, request); its keys are chunks of 32 tokens (two
+// tiles). All units' chunks in a row, each unit with
 // kCaLead chunks' worth of fixed work before them, are cut in equal shares, one per
 // warp, from the lengths on the device: ragged batches and single long requests
 // balance alike, and a captured call follows its lengths. A warp's part of a unit is
@@ -48,20 +51,13 @@
 // records and applies S H / d.
 #pragma once
 
-#include "kvc_attend_mma.cuh"
-#include "kvc_cache.h"
-#include "kvc_launch.cuh"
+#include "kvc_cache_combine.cuh"
 
 namespace kvc {
 
 constexpr int kChunkTok = 2 * kTileTok;
 constexpr uint32_t kCaLead = 2;      // a segment's fixed work, in chunks
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // Transposes an 8 x 8 matrix of 16-bit values held as a fragment.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t y;
@@ -73,108 +69,25 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// n - 8 of the codes in bits 0..3 (kHigh: 4..7) of both halves, as fp16 pairs.
-template <bool kHigh>
-__device__ __forceinline__ uint32_t centred(uint32_t x) {
-  uint32_t t, d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
-      : "=r"(t)
-      : "r"(x), "n"(kHigh ? 0x00F000F0 : 0x000F000F), "n"(kHigh ? 0x54005400 : 0x64006400));
-  asm("sub.f16x2 %0, %1, %2;" : "=r"(d) : "r"(t), "r"(kHigh ? 0x54805480u : 0x64086408u));
-  return d;
-}
-__device__ __forceinline__ float half_lo(uint32_t m) {
-  return __half2float(__ushort_as_half(uint16_t(m)));
-}
-__device__ __forceinline__ float half_hi(uint32_t m) {
-  return __half2float(__ushort_as_half(uint16_t(m >> 16)));
-}
-// Whether a meta word's scale or zero is infinite or NaN.
-__device__ __forceinline__ bool not_finite(uint32_t m) {
-  return (m & 0x7C00u) == 0x7C00u || (m & 0x7C000000u) == 0x7C000000u;
-}
-// A meta word's z + 8 s.
-__device__ __forceinline__ float zero8(uint32_t m) { return fmaf(8.f, half_lo(m), half_hi(m)); }
-
-// A request from the host's limits and its device numbers: queries, their first
-// row, keys, and (from them) the first chunk that some query sees, chunks. One out of
-// range has no queries.
-struct ReqShape {
-  uint32_t nq, q0, len, chunk0, chunks;
+// The chunks of keys that some query of a request sees, from the first one on.
+struct KeyChunks {
+  uint32_t first, count;
 };
-__device__ __forceinline__ ReqShape shape_from(const CacheAttnArgs &a, uint32_t nq, uint32_t q0,
-                                               uint32_t len) {
-  ReqShape s{nq, q0, len, 0, 0};
-  if (nq == 0 || len == 0) return s;
-  const int64_t lo = a.window ? int64_t(len) - int64_t(nq) - int64_t(a.window) + 1 : 0;
-  s.chunk0 = lo > 0 ? uint32_t(lo) / kChunkTok : 0;
-  s.chunks = (len + kChunkTok - 1) / kChunkTok - s.chunk0;
-  return s;
-}
-// From the caller's arrays; ok: in range.
-__device__ __forceinline__ ReqShape read_request(const CacheAttnArgs &a, uint32_t r, bool &ok) {
-  const int64_t q0 = a.q_starts ? int64_t(__ldg(a.q_starts + r)) : int64_t(r);
-  const int64_t q1 = a.q_starts ? int64_t(__ldg(a.q_starts + r + 1)) : int64_t(r) + 1;
-  const int64_t len = __ldg(a.seq_lens + r);
-  ok = q0 >= 0 && q1 >= q0 && q1 <= int64_t(a.q_tokens) && q1 - q0 <= int64_t(a.max_q) &&
-       len >= 0 && len <= int64_t(a.max_len);
-  return ok ? shape_from(a, uint32_t(q1 - q0), uint32_t(q0), uint32_t(len)) : ReqShape{};
-}
-// From the first kernel's copy in the workspace.
-__device__ __forceinline__ ReqShape request_shape(const CacheAttnArgs &a, uint32_t r) {
-  const uint4 v = a.shapes[r];
-  return shape_from(a, v.x, v.y, v.z);
-}
-// Keys [lo, hi) that query i of a request sees.
-__device__ __forceinline__ void key_range(const CacheAttnArgs &a, const ReqShape &s, uint32_t i,
-                                          int32_t &lo, int32_t &hi) {
-  const int64_t end = a.causal ? int64_t(s.len) - int64_t(s.nq) + int64_t(i) + 1 : int64_t(s.len);
-  const int64_t beg = a.window ? end - int64_t(a.window) : 0;
-  hi = int32_t(end > 0 ? end : 0);
-  lo = int32_t(beg > 0 ? beg : 0);
-}
-
-// a / b, in 32 bits where they suffice (most calls).
-__device__ __forceinline__ uint64_t div64(uint64_t a, uint64_t b) {
-  return ((a | b) >> 32) == 0 ? uint64_t(uint32_t(a) / uint32_t(b)) : a / b;
-}
-// Blocks of query rows are numbered so that no request has to know the others: the
-// first of request r is floor(q0 q_per_kv / COLS) + r, which leaves each its own
-// numbers below max_blocks. Units: (l * heads + h) * max_blocks + block, increasing
-// in the order of the work.
-template <int COLS>
-__device__ __forceinline__ uint32_t first_block(const CacheAttnArgs &a, uint32_t q0, uint32_t r) {
-  return q0 * a.qpk / COLS + r;
-}
-template <int COLS>
-__device__ __forceinline__ uint32_t blocks_of(const CacheAttnArgs &a, const ReqShape &s) {
-  return (s.nq * a.qpk + COLS - 1) / COLS;
+__device__ __forceinline__ KeyChunks key_chunks(const CacheAttnArgs &a, const ReqShape &s) {
+  if (s.nq == 0 || s.len == 0) return KeyChunks{0, 0};
+  const int64_t lo = a.window ? int64_t(s.len) - int64_t(s.nq) - int64_t(a.window) + 1 : 0;
+  const uint32_t first = lo > 0 ? uint32_t(lo) / kChunkTok : 0;
+  return KeyChunks{first, (s.len + kChunkTok - 1) / kChunkTok - first};
 }
 // A unit's work: its chunks, and kCaLead before them; none without chunks.
-__device__ __forceinline__ uint32_t unit_work(const ReqShape &s) {
-  return s.chunks ? s.chunks + kCaLead : 0;
+__device__ __forceinline__ uint32_t unit_work(const KeyChunks &k) {
+  return k.count ? k.count + kCaLead : 0;
 }
 // Warp g (of all CTAs) takes the work [g * share, (g + 1) * share) of all units'
 // in a row.
 __device__ __forceinline__ uint64_t work_per_warp(uint64_t total, uint32_t warps) {
   return div64(total + warps - 1, warps);
 }
-// The largest r < n with in(r), for an in() that is true up to some r and false
-// after it (0 if it is false at once). The warp looks at 32 places at a time.
-template <class In>
-__device__ __forceinline__ uint32_t last_with(uint32_t n, In in) {
-  const uint32_t lane = threadIdx.x & 31;
-  uint32_t lo = 0, len = n;
-  while (len > 1) {
-    const uint32_t step = (len + 31) / 32, p = lane * step;
-    const uint32_t yes = __ballot_sync(0xFFFFFFFFu, p < len && in(lo + p));
-    const uint32_t k = yes ? 31 - __clz(yes) : 0;
-    lo += k * step;
-    len = min(step, len - k * step);
-  }
-  return lo;
-}
-
 template <int D, int G, int NB>
 struct CaCfg {
   static constexpr int NG = D / G;
@@ -219,22 +132,17 @@ __global__ void __launch_bounds__(kCaPrepWarps * 32)
   const uint32_t n = a.n_req, H = a.c.heads;
   if (blockIdx.x == 0) {
     __shared__ uint64_t red[kCaPrepWarps];
-    __shared__ uint32_t down;
-    if (tid == 0) down = 0;
-    __syncthreads();
     const uint32_t per = (n + T - 1) / T, r0 = uint32_t(tid) * per, r1 = min(n, r0 + per);
     uint64_t w = 0;
-    bool bad = false, falls = false;
+    bool bad = false;
     for (uint32_t r = r0; r < r1; ++r) {
       bool ok;
       const ReqShape s = read_request(a, r, ok);
       bad |= !ok;
-      if (a.q_starts) falls |= __ldg(a.q_starts + r + 1) < __ldg(a.q_starts + r);
       a.shapes[r] = make_uint4(s.nq, s.q0, s.len, 0);
-      w += uint64_t(unit_work(s)) * blocks_of<COLS>(a, s);
+      w += unit_work(key_chunks(a, s));
     }
     if (bad && a.status) set_status(a.status, KVC_ERR_CORRUPT);
-    if (falls) down = 1;
     uint64_t wi = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -243,36 +151,26 @@ __global__ void __launch_bounds__(kCaPrepWarps * 32)
     }
     if (lane == 31) red[warp] = wi;
     __syncthreads();
-    // q_starts that decrease: rows of one request may be another's, so none is served
-    const bool none = down != 0;
     uint64_t base = wi - w;
     for (int k = 0; k < warp; ++k) base += red[k];
     for (uint32_t r = r0; r < r1; ++r) {
-      a.wpre[r] = none ? 0 : base;
+      a.wpre[r] = base;
       const uint4 v = a.shapes[r];
-      const ReqShape s = shape_from(a, v.x, v.y, v.z);
-      if (none) a.shapes[r] = make_uint4(0, 0, 0, 0);
-      base += uint64_t(unit_work(s)) * blocks_of<COLS>(a, s);
+      base += unit_work(key_chunks(a, ReqShape{v.x, v.y, v.z}));
     }
-    if (tid == T - 1) a.wpre[n] = none ? 0 : base;
+    if (tid == T - 1) a.wpre[n] = base;
     return;
   }
-  const uint32_t unit = blockIdx.x - 1, lh = unit / a.max_blocks, block = unit - lh * a.max_blocks;
+  const uint32_t unit = blockIdx.x - 1, lh = unit / n, r = unit - lh * n;
   const uint32_t l = lh / H, h = lh - l * H;
-  // the request whose block this is: the last whose first block is not past it
-  const uint32_t lo = last_with(n, [&](uint32_t r) {
-    const uint32_t q0 = a.q_starts ? uint32_t(max(0, __ldg(a.q_starts + r))) : r;
-    return first_block<COLS>(a, q0, r) <= block;
-  });
   bool ok;
-  const ReqShape rs = read_request(a, lo, ok);
-  const uint32_t fb = first_block<COLS>(a, rs.q0, lo);
-  if (!ok || rs.chunks == 0 || block < fb || block - fb >= blocks_of<COLS>(a, rs)) return;
-  const uint32_t c0 = (block - fb) * COLS, rows = rs.nq * a.qpk;
+  const ReqShape rs = read_request(a, r, ok);
+  if (!ok || key_chunks(a, rs).count == 0) return;
+  const uint32_t rows = rs.nq * a.qpk;
   __shared__ alignas(16) uint8_t frag[C::QB];
   for (int col = warp; col < COLS; col += kCaPrepWarps) {
-    const bool live = c0 + col < rows;
-    const uint32_t row = c0 + (live ? col : 0), qi = row / a.qpk;
+    const bool live = uint32_t(col) < rows;
+    const uint32_t row = live ? col : 0, qi = row / a.qpk;
     const uint8_t *src = a.q + int64_t(l) * a.q_l + int64_t(rs.q0 + qi) * a.q_t +
                          int64_t(h * a.qpk + (row - qi * a.qpk)) * a.q_h;
     uint16_t in[C::W];
@@ -364,7 +262,7 @@ __global__ void __launch_bounds__(kCaPrepWarps * 32)
 
 // A warp's part of a unit.
 struct Segment {
-  uint32_t l, h, r, c0, nc;      // layer, kv head, request; the unit's query rows
+  uint32_t l, h, r, nc;          // layer, kv head, request; its query rows
   uint32_t first, chunks;        // the segment's chunks
   uint64_t unit, u0, u1;         // the unit, and its work [u0, u1)
   int32_t any_lo, any_hi, all_lo, all_hi;  // keys that some row sees, that every row sees
@@ -372,7 +270,6 @@ struct Segment {
 };
 // The segment at f, the place of the next one (as f). chunks may be 0: the share
 // ends inside a unit's fixed work.
-template <int COLS>
 __device__ __forceinline__ Segment segment_at(const CacheAttnArgs &a, const uint64_t *wpre,
                                               uint64_t f_end, uint64_t &f) {
   const uint32_t n = a.n_req;
@@ -383,23 +280,21 @@ __device__ __forceinline__ Segment segment_at(const CacheAttnArgs &a, const uint
   const uint32_t lo = last_with(n, [&](uint32_t r) { return wpre[r] <= in_lh; });
   s.r = lo;
   s.rs = request_shape(a, lo);
-  const uint32_t work = unit_work(s.rs);
-  const uint64_t in_r = in_lh - wpre[lo];
-  const uint32_t block = uint32_t(div64(in_r, work));
-  s.c0 = block * COLS;
-  s.nc = min(uint32_t(COLS), s.rs.nq * a.qpk - s.c0);
-  s.unit = lh * a.max_blocks + first_block<COLS>(a, s.rs.q0, lo) + block;
-  const uint32_t at = uint32_t(in_r - uint64_t(block) * work);
+  const KeyChunks kc = key_chunks(a, s.rs);
+  const uint32_t work = unit_work(kc);
+  s.nc = s.rs.nq * a.qpk;
+  s.unit = lh * n + lo;
+  const uint32_t at = uint32_t(in_lh - wpre[lo]);
   const uint32_t end = uint32_t(min(uint64_t(work), at + (f_end - f)));
   const uint32_t c_at = at > kCaLead ? at - kCaLead : 0, c_end = end > kCaLead ? end - kCaLead : 0;
-  s.first = s.rs.chunk0 + c_at;
+  s.first = kc.first + c_at;
   s.chunks = c_end - c_at;
   s.u0 = f - at;
   s.u1 = s.u0 + work;
   f += end - at;
   // rows are ordered by query
-  key_range(a, s.rs, s.c0 / a.qpk, s.any_lo, s.all_hi);
-  key_range(a, s.rs, (s.c0 + s.nc - 1) / a.qpk, s.all_lo, s.any_hi);
+  key_range(a, s.rs, 0, s.any_lo, s.all_hi);
+  key_range(a, s.rs, s.rs.nq - 1, s.all_lo, s.any_hi);
   return s;
 }
 
@@ -441,7 +336,7 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
     // a warp with nothing to do still looks whether it is to take part in a merge
     const bool idle = f >= f_end;
     uint64_t next = idle ? cta1 - 1 : f;
-    Segment s = segment_at<COLS>(a, wpre, idle ? cta1 : f_end, next);
+    Segment s = segment_at(a, wpre, idle ? cta1 : f_end, next);
     if (idle) s.chunks = 0;
     f = next;
     // The CTA's whole share in one unit: its warps are merged to one record.
@@ -621,7 +516,7 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
 #pragma unroll
           for (int i = 0; i < R; ++i) {
             lim[i] = make_int2(0, 0);
-            if (uint32_t(row_of(i)) < s.nc) key_range(a, s.rs, (s.c0 + row_of(i)) / a.qpk, lim[i].x, lim[i].y);
+            if (uint32_t(row_of(i)) < s.nc) key_range(a, s.rs, row_of(i) / a.qpk, lim[i].x, lim[i].y);
           }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
@@ -852,144 +747,39 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
   } while (f < f_end);
 }
 
-// Brings sums (L, y) under maximum M to maximum top >= M.
-__device__ __forceinline__ void merge_scale(float &M, float &L, float top, float (&y)[4]) {
-  if (M != -INFINITY && M != top) {
-    const float k = ex2(M - top);
-    L *= k;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] *= k;
-  }
-  M = top;
-}
-
-// A row's records in turn, or split between WPR warps (few units, many records
-// each): their merge, then S H / d.
-template <int D, int COLS, int CW, int DT, int WPR>
-__global__ void __launch_bounds__(WPR == 1 ? 128 : WPR * 32)
-    cache_combine_kernel(const __grid_constant__ CacheAttnArgs a, const uint32_t grid) {
-  constexpr int W = D / 32;
-  __shared__ float part[WPR == 1 ? 1 : WPR][WPR == 1 ? 1 : D];
-  __shared__ float2 ml[WPR];
-  grid_dependency_wait();  // the records and the prefixes
-  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, H = a.c.heads, Hq = H * a.qpk;
-  const uint64_t i = WPR == 1 ? uint64_t(blockIdx.x) * 4 + warp : uint64_t(blockIdx.x);
-  if (i >= uint64_t(a.c.layers) * a.q_tokens * Hq) return;
-  const uint32_t n = a.n_req;
-  const uint64_t lt = div64(i, Hq);
-  const uint32_t j = uint32_t(i - lt * Hq), l = uint32_t(div64(lt, a.q_tokens));
-  const uint32_t tok = uint32_t(lt - uint64_t(l) * a.q_tokens);
-  uint32_t r = tok;
-  if (a.q_starts) r = last_with(n + 1, [&](uint32_t x) { return __ldg(a.q_starts + x) <= int32_t(tok); });
-  if (r >= n) return;
-  const ReqShape rs = request_shape(a, r);
-  if (tok < rs.q0 || tok - rs.q0 >= rs.nq) return;  // a row that no request names
-  const uint32_t h = j / a.qpk, row = (tok - rs.q0) * a.qpk + (j - h * a.qpk);
-  float y[4] = {0.f, 0.f, 0.f, 0.f}, M = -INFINITY, L = 0.f;
-  if (rs.chunks) {
-    const uint32_t block = row / COLS, work = unit_work(rs);
+// A row's records: one per warp that has some of the unit's chunks, one only for a CTA
+// whose share lies in the unit (its first warp's).
+template <int C_, int CW>
+struct DecodeRecords {
+  static constexpr int COLS = C_;
+  uint64_t unit = 0;
+  uint32_t row = 0, nrec = 0, n0 = 0, s0 = 0, b0 = 0, b1 = 0;
+  __device__ __forceinline__ DecodeRecords(const CacheAttnArgs &a, uint32_t grid, const ReqShape &q,
+                                           uint32_t l, uint32_t h, uint32_t r, uint32_t row_) {
+    const KeyChunks kc = key_chunks(a, q);
+    if (kc.count == 0) return;
+    const uint32_t n = a.n_req, H = a.c.heads, work = unit_work(kc);
     const uint64_t lh = uint64_t(l) * H + h, per_lh = a.wpre[n], total = per_lh * H * a.c.layers;
     const uint64_t share = work_per_warp(total, grid * CW), cta = share * CW;
-    const uint64_t unit = lh * a.max_blocks + first_block<COLS>(a, rs.q0, r) + block;
     // the unit's work [u0, u1), its chunks from u0 + kCaLead; the warps that have them
-    const uint64_t u0 = lh * per_lh + a.wpre[r] + uint64_t(block) * work, u1 = u0 + work;
+    const uint64_t u0 = lh * per_lh + a.wpre[r], u1 = u0 + work;
     const uint32_t g0 = uint32_t(div64(u0 + kCaLead, share)), g1 = uint32_t(div64(u1 - 1, share));
-    const uint32_t b0 = g0 / CW, b1 = g1 / CW;
-    // CTAs whose share lies in the unit have one record (their first warp's), the
-    // others one per warp
+    unit = lh * n + r;
+    row = row_;
+    b0 = g0 / CW;
+    b1 = g1 / CW;
     const bool m0 = uint64_t(b0) * cta >= u0 && min(total, (uint64_t(b0) + 1) * cta) <= u1;
     const bool m1 = uint64_t(b1) * cta >= u0 && min(total, (uint64_t(b1) + 1) * cta) <= u1;
-    const uint32_t n0 = m0 ? 1 : min(g1, b0 * CW + CW - 1) - g0 + 1;  // of the first CTA
-    const uint32_t nrec = n0 + (b1 > b0 ? (b1 - b0 - 1) + (m1 ? 1 : g1 - b1 * CW + 1) : 0);
-    const uint32_t s0 = m0 ? b0 * CW : g0;
-    auto warp_at = [&](uint32_t k) -> uint32_t {
-      if (k < n0) return s0 + k;
-      k -= n0;
-      return k < b1 - b0 - 1 ? (b0 + 1 + k) * CW : b1 * CW + (k - (b1 - b0 - 1));
-    };
-    constexpr uint32_t kStep = COLS * (4 + D);
-    const float *p0 = a.rec + unit * uint64_t(kStep) + (row - block * COLS) * (4 + D);
-    // four records at a time: their loads first, then the running maximum and sums
-    for (uint32_t k0 = WPR == 1 ? 0 : 4 * warp; k0 < nrec; k0 += 4 * WPR) {
-      float2 v[4];
-      float o[4][W];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool in = k0 + e < nrec;
-        const float *p = p0 + uint64_t(warp_at(in ? k0 + e : k0)) * kStep;
-        v[e] = in ? *reinterpret_cast<const float2 *>(p) : make_float2(-INFINITY, 0.f);
-#pragma unroll
-        for (int c = 0; c < W; ++c) o[e][c] = p[4 + lane + 32 * c];
-      }
-      const float top = fmaxf(M, fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x)));
-      merge_scale(M, L, top, y);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (v[e].x == -INFINITY && v[e].y == 0.f) continue;  // no key of this row in the segment
-        const float w = v[e].x == -INFINITY ? 1.f : ex2(v[e].x - top);
-        L = fmaf(w, v[e].y, L);
-#pragma unroll
-        for (int c = 0; c < W; ++c) y[c] = fmaf(w, o[e][c], y[c]);
-      }
-    }
+    n0 = m0 ? 1 : min(g1, b0 * CW + CW - 1) - g0 + 1;  // of the first CTA
+    nrec = n0 + (b1 > b0 ? (b1 - b0 - 1) + (m1 ? 1 : g1 - b1 * CW + 1) : 0);
+    s0 = m0 ? b0 * CW : g0;
   }
-  if constexpr (WPR > 1) {  // in the warps' order
-#pragma unroll
-    for (int c = 0; c < W; ++c) part[warp][lane + 32 * c] = y[c];
-    if (lane == 0) ml[warp] = make_float2(M, L);
-    __syncthreads();
-    if (warp) return;
-#pragma unroll
-    for (int w = 1; w < WPR; ++w) M = fmaxf(M, ml[w].x);
-    L = 0.f;
-#pragma unroll
-    for (int c = 0; c < W; ++c) y[c] = 0.f;
-#pragma unroll
-    for (int w = 0; w < WPR; ++w) {
-      const float2 v = ml[w];
-      if (v.x == -INFINITY && v.y == 0.f) continue;
-      const float k = v.x == -INFINITY ? 1.f : ex2(v.x - M);
-      L = fmaf(k, v.y, L);
-#pragma unroll
-      for (int c = 0; c < W; ++c) y[c] = fmaf(k, part[w][lane + 32 * c], y[c]);
-    }
+  __device__ __forceinline__ uint32_t id(uint32_t k) const {
+    if (k < n0) return s0 + k;
+    k -= n0;
+    return k < b1 - b0 - 1 ? (b0 + 1 + k) * CW : b1 * CW + (k - (b1 - b0 - 1));
   }
-  const bool empty = M == -INFINITY && L == 0.f;
-#pragma unroll
-  for (int s = 1; s < 32; s <<= 1)
-#pragma unroll
-    for (int c = 0; c < W; ++c) {
-      const float o = __shfl_xor_sync(0xFFFFFFFFu, y[c], s);
-      y[c] = (lane & s) ? o - y[c] : y[c] + o;
-    }
-#pragma unroll
-  for (int s = 1; s < W; s <<= 1)
-#pragma unroll
-    for (int c = 0; c < W; ++c)
-      if ((c & s) == 0) {
-        const float u = y[c], v = y[c + s];
-        y[c] = u + v;
-        y[c + s] = u - v;
-      }
-  uint64_t w0 = a.c.w0, w1 = a.c.w1;
-  if (a.c.vec_signs) {  // the values' diagonal
-    uint64_t st = a.c.seed + ((uint64_t(l) * 2 + 1) * H + h) * uint64_t(D / 64) * 0x9E3779B97F4A7C15ull;
-    w0 = splitmix64(st);
-    if constexpr (D == 128) w1 = splitmix64(st);
-  }
-  const float f = empty ? 0.f : 1.f / (L * float(D));
-  uint16_t *out = reinterpret_cast<uint16_t *>(a.out + int64_t(l) * a.o_l + int64_t(tok) * a.o_t +
-                                               int64_t(j) * a.o_h);
-#pragma unroll
-  for (int c = 0; c < W; ++c) {
-    const uint32_t sg = uint32_t((c < 2 ? w0 : w1) >> (32 * (c & 1) + lane)) & 1u;
-    const float x = empty ? 0.f : __uint_as_float(__float_as_uint(y[c] * f) ^ (sg << 31));
-    out[lane + 32 * c] = DT == KVC_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x))
-                                        : __half_as_ushort(__float2half_rn(x));
-  }
-  if (a.lse && lane == 0)
-    a.lse[lt * Hq + j] = empty ? -INFINITY : fmaf(M, 0.693147180559945f, logf(L));
-}
+};
 
 template <int D, int G, int NB>
 cudaError_t cache_attend_t(int dtype, const CacheAttnArgs &a, int sms, cudaStream_t st) {
@@ -1007,7 +797,7 @@ cudaError_t cache_attend_t(int dtype, const CacheAttnArgs &a, int sms, cudaStrea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.stream = st;
-  const uint64_t units = uint64_t(a.c.layers) * a.c.heads * a.max_blocks;
+  const uint64_t units = uint64_t(a.c.layers) * a.c.heads * a.n_req;
   cache_attend_prep_kernel<D, G, NB><<<unsigned(units + 1), kCaPrepWarps * 32, 0, st>>>(a, dtype);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -1019,27 +809,15 @@ cudaError_t cache_attend_t(int dtype, const CacheAttnArgs &a, int sms, cudaStrea
   if (e != cudaSuccess) return e;
   // one warp per row where units are as many as CTAs (a row then has one or two
   // records), eight where a unit is spread over many CTAs
-  const uint64_t rows = uint64_t(a.c.layers) * a.q_tokens * a.c.heads * a.qpk;
-  const bool wide = uint64_t(a.c.layers) * a.n_req * a.c.heads * 4 < grid;
-  const uint64_t cg = wide ? rows : (rows + 3) / 4;
-  if (cg >= (uint64_t(1) << 31)) return cudaErrorInvalidValue;
-  auto ck = dtype == KVC_BF16 ? (wide ? cache_combine_kernel<D, C::COLS, C::CW, KVC_BF16, 8>
-                                      : cache_combine_kernel<D, C::COLS, C::CW, KVC_BF16, 1>)
-                              : (wide ? cache_combine_kernel<D, C::COLS, C::CW, KVC_FP16, 8>
-                                      : cache_combine_kernel<D, C::COLS, C::CW, KVC_FP16, 1>);
-  cfg.gridDim = dim3(unsigned(cg));
-  cfg.blockDim = dim3(wide ? 256 : 128);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, ck, a, grid);
+  return launch_combine<D, DecodeRecords<C::COLS, C::CW>>(dtype, units * 4 < grid, a, grid, st);
 }
 
 template <int D, int G>
 cudaError_t cache_attend_g(int dtype, const CacheAttnArgs &a, int sms, cudaStream_t st) {
-  switch (cache_cols(uint64_t(a.max_q) * a.qpk)) {
-    case 4: return cache_attend_t<D, G, 1>(dtype, a, sms, st);
-    case 8: return cache_attend_t<D, G, 2>(dtype, a, sms, st);
-    default: return cache_attend_t<D, G, 4>(dtype, a, sms, st);
-  }
+  const uint64_t rows = uint64_t(a.max_q) * a.qpk;
+  if (rows <= 4) return cache_attend_t<D, G, 1>(dtype, a, sms, st);
+  if (rows <= 8) return cache_attend_t<D, G, 2>(dtype, a, sms, st);
+  return cache_attend_t<D, G, 4>(dtype, a, sms, st);
 }
 
 }  // namespace kvc

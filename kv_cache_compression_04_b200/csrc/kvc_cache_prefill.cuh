@@ -4,27 +4,28 @@
 // kvc_cache_attend.cuh; the codes stay exact in the score product.
 //
 // A unit is (layer, kv head, block of 128 query rows of a request: row = query *
-// q_per_kv + head), its keys are tiles of NK = 128 / (groups per vector). Per tile:
-//   S_g = (Q hi + Q lo)_g (n - 8)_g^T   a 128 x NK accumulator for each group g, NG of
-//         them in 128 columns: scores are s_g S_g + (z + 8 s)_g sum(Q_g), which keeps
-//         codes and queries (22 bits) exact where keys rounded to fp16 would not be;
-//   P     = softmax weights in fp16, written to tensor memory as the next product's
-//         operand;
+// q_per_kv + head), its keys are tiles of NK = 64 (32 with four groups). Per tile:
+//   S_g = (Q hi + Q lo)_g (n - 8)_g^T   a 128 x NK accumulator for each group g: scores
+//         are s_g S_g + (z + 8 s)_g sum(Q_g), which keeps codes and queries (22 bits)
+//         exact where keys rounded to fp16 would not be;
+//   P     = softmax weights in fp16, written to tensor memory (over the scores) as the
+//         next product's operand;
 //   O    += P V, V dequantised to fp16 (rounded once, as P is): 128 x D.
-// Floor per 128 x 128 tile pair at d = 128: 3 x 512 cycles of the tensor cores (hi and
-// lo parts, values).
+// Floor per 128 x 64 tile pair at d = 128: 3 x 256 cycles of the tensor cores (hi and
+// lo parts, values); the scores' operands come from shared memory and take 1.5 times that.
 //
-// Warps 0..7: softmax. Warp w has rows 32 (w % 4) .. + 31 (a thread per row, as tensor
-// memory is read) and half w / 4 of the tile's keys; the halves' maxima meet in
-// shared memory. Thread 0 starts the products: tile j + 2's scores and tile j's
-// values once tile j's weights are written, so that the tensor cores work on the
-// next tile's scores during a softmax. Warps 8..11: unpack the tiles, two ahead.
+// Warps 0..3 do the even tiles' softmax, 4..7 the odd ones', a thread per row with a
+// maximum, a sum and an output accumulator of its own: the two never wait for each other,
+// and one's exponentials run beside the other's products. Their results meet at a
+// segment's end. Warps 8..11 unpack the even tiles, 12..15 the odd ones, up to four
+// tiles ahead. Warp 16 starts the products: a start waits while the tensor cores' queue
+// is full, which would hold up a softmax warp.
 // Work is shared out as in kvc_cache_attend.cuh, a share per CTA (one per SM).
 //
 // Shared memory, 128-byte swizzle (16-byte piece c of row r at c ^ (r & 7)):
 //   Q: hi, lo; 64-channel slabs of 128 rows x 128 bytes (K-major)
 //   K: 64-channel slabs of NK rows x 128 bytes (K-major), V: the same (N-major: a row
-//   is a token, its channels are the product's columns), two buffers each.
+//   is a token, its channels are the product's columns), four stages each.
 // Eight codes of a word come apart as (0, 4), (1, 5), (2, 6), (3, 7): channels of Q
 // follow that order, and output columns are put in order when they are written.
 #pragma once
@@ -34,29 +35,34 @@
 namespace kvc {
 
 constexpr int kPfRows = 128;
-constexpr int kPfSoft = 256, kPfUnpack = 128, kPfThreads = kPfSoft + kPfUnpack;
+constexpr int kPfSoft = 256, kPfUnpack = 256, kPfThreads = kPfSoft + kPfUnpack + 128;
+// Registers: 640 threads start with 96 each; the softmax warps take 144, the unpacking
+// ones keep 72 and the last four 48 (2 x 128 x (144 + 72) + 128 x 48 = 640 x 96).
+constexpr int kPfSoftRegs = 144, kPfUnpackRegs = 72, kPfIssueRegs = 48;
+constexpr uint32_t kPfStages = 4;
 constexpr uint32_t kPfLead = 3;  // a segment's fixed work, in tiles
 
 template <int D, int G>
 struct PfCfg {
-  static constexpr int NG = D / G, NK = 128 / NG, SL = D / 64, W = D / 32;
+  static constexpr int NG = D / G, NK = NG == 4 ? 32 : 64, SL = D / 64, W = D / 32;
   static constexpr uint32_t TB = cache_tile_bytes(D, G), CB = cache_code_bytes(D);
   static constexpr uint32_t QPART = SL * kPfRows * 128, KBUF = SL * NK * 128;
   static constexpr int MW = 2 * NG + 2;  // words of a key's numbers: s, z + 8 s; 2^e, bias
   static constexpr size_t q = 0;
   static constexpr size_t k = q + 2 * QPART;
-  static constexpr size_t v = k + 2 * KBUF;
-  static constexpr size_t meta = v + 2 * KBUF;
-  static constexpr size_t fc = meta + 2 * size_t(MW) * NK * 4;
+  static constexpr size_t v = k + kPfStages * KBUF;
+  static constexpr size_t meta = v + kPfStages * KBUF;
+  static constexpr size_t fc = meta + kPfStages * size_t(MW) * NK * 4;
   static constexpr size_t qs = fc + kPfRows * 4;
-  static constexpr size_t mx = qs + size_t(NG) * kPfRows * 4;
-  static constexpr size_t wmax = mx + 2 * 2 * kPfRows * 4;  // [buffer][unpacking warp]
-  static constexpr size_t wodd = wmax + 2 * 4 * 4;
-  static constexpr size_t bars = wodd + 2 * 4 * 4;          // full, scores, values: two each
-  static constexpr size_t ctl = bars + 6 * 8;               // tensor memory, dead
+  static constexpr size_t fin = qs + size_t(NG) * kPfRows * 4;  // [softmax][row] maximum, sum
+  static constexpr size_t wmax = fin + 2 * kPfRows * 8;         // [stage][unpacking warp]
+  static constexpr size_t wodd = wmax + kPfStages * 4 * 4;
+  // full and values (a stage), scores and weights (a softmax), queries
+  static constexpr size_t bars = wodd + kPfStages * 4 * 4;
+  static constexpr size_t ctl = bars + (2 * kPfStages + 5) * 8 + 8;  // tensor memory, dead
   static constexpr size_t bytes = ctl + 16;
-  // columns of tensor memory: scores 2 x 128, weights 2 x 64, output
-  static constexpr uint32_t tS = 0, tP = 256, tO = 384;
+  // columns of tensor memory: scores and weights 2 x 128, outputs 2 x 128
+  static constexpr uint32_t tS = 0, tO = 256;
   static_assert(bars % 8 == 0 && fc % 16 == 0 && bytes + 1024 <= 227 * 1024, "shared memory");
 };
 
@@ -130,6 +136,16 @@ __device__ __forceinline__ void tm_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(add)
       : "memory");
+}
+// One lane of a converged warp: the compiler then knows that one thread issues, and takes
+// the operands from uniform registers at once.
+__device__ __forceinline__ bool tm_elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ uint32_t tm_uniform(uint32_t x) {  // x is the same in all lanes
+  return __reduce_max_sync(0xFFFFFFFFu, x);
 }
 __device__ __forceinline__ void tm_commit(uint64_t *bar) {
   asm volatile(
@@ -248,66 +264,87 @@ __device__ __forceinline__ PfSegment pf_segment_at(const CacheAttnArgs &a, uint6
   return s;
 }
 
-// Unpacking warps: tile after tile of every segment into the two buffers.
+// A thread's part of a tile as it is stored: pieces p of RX rows' keys and values.
 template <int D, int G>
-__device__ __forceinline__ void pf_unpack(const CacheAttnArgs &a, uint8_t *smem, uint64_t f,
-                                          uint64_t f_end) {
+struct PfRaw {
+  static constexpr int NG = D / G, W = D / 32, RX = PfCfg<D, G>::NK / 32;
+  uint32_t k[RX][W], v[RX][W], mk[RX][NG], mv[RX][NG];
+  bool in[RX];
+};
+
+// Unpacking warps: every second tile of the CTA's share (odd: which). A thread has
+// piece t % 4 of rows r0 + 32 x; rows r and r + 4 share a quarter-warp, whose stores
+// then meet different banks. The next tile's rows are asked for as soon as a tile is
+// unpacked, with pages looked up a tile earlier.
+template <int D, int G>
+__device__ __forceinline__ void pf_unpack(const CacheAttnArgs &a, uint8_t *smem,
+                                          uint32_t which, uint64_t f, uint64_t f_end) {
   using C = PfCfg<D, G>;
-  constexpr int NG = C::NG, NK = C::NK, W = C::W, RX = NK / 32;
-  const uint32_t t = threadIdx.x - kPfSoft, lane = t & 31, warp = t >> 5, p = t & 3, r0 = t >> 2;
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::bars), *pv = full + 4;
+  using Raw = PfRaw<D, G>;
+  constexpr int NG = C::NG, NK = C::NK, W = C::W, RX = Raw::RX;
+  const uint32_t t = threadIdx.x & 127, lane = t & 31, warp = t >> 5, p = t & 3;
+  const uint32_t r0 = 8 * warp + 4 * ((t >> 2) & 1) + ((t >> 3) & 3);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::bars), *pv = full + kPfStages;
   volatile uint32_t *dead = reinterpret_cast<uint32_t *>(smem + C::ctl) + 1;
-  uint32_t j = 0;
-  while (f < f_end) {
+  uint32_t j0 = 0;  // tiles before the segment
+  for (uint32_t tiles = 0; f < f_end; j0 += tiles) {
     const PfSegment s = pf_segment_at(a, f_end, f);
+    tiles = s.tiles;
+    const uint32_t i0 = (which ^ j0) & 1u;  // the segment's first tile of these warps
+    if (i0 >= tiles) continue;
     const uint8_t *base = a.c.pool + int64_t(s.l) * a.c.s_l + int64_t(s.h) * a.c.s_h;
     const int32_t *table = a.page_table + int64_t(s.r) * a.pt_stride;
-    uint32_t k[RX][W], v[RX][W], mk[RX][NG], mv[RX][NG];
-    bool in[RX];
-    auto load = [&](uint32_t tile) {
+    int32_t pg[RX];  // pages of the next tile's rows, -1: no row sees the key
+    auto look = [&](uint32_t i) {
 #pragma unroll
       for (int x = 0; x < RX; ++x) {
-        const int32_t tok = int32_t(tile * NK + r0 + 32 * x);
-        in[x] = tok >= s.any_lo && tok < s.any_hi;
-        const uint8_t *src = nullptr;
-        if (in[x]) {
-          const uint32_t kt = uint32_t(tok) / kTileTok, pi = fdiv(a.tpp, kt);
-          const int32_t pg = __ldg(table + pi);
-          in[x] = pg >= 0 && uint32_t(pg) < a.c.num_pages;
-          if (in[x])
-            src = base + int64_t(pg) * a.c.s_p + int64_t(kt - pi * a.tpp.d) * C::TB;
-          else if (a.status)
-            set_status(a.status, KVC_ERR_CORRUPT);
+        const int32_t tok = int32_t((s.first + i) * NK + r0 + 32 * x);
+        pg[x] = -1;
+        if (i < s.tiles && tok >= s.any_lo && tok < s.any_hi) {
+          pg[x] = __ldg(table + fdiv(a.tpp, uint32_t(tok) / kTileTok));
+          pg[x] = pg[x] < 0 ? -2 : pg[x];
         }
-        const uint32_t ln = uint32_t(tok) % kTileTok;
+      }
+    };
+    auto load = [&](Raw &w, uint32_t i) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) k[x][i] = v[x][i] = 0x88888888u;  // n - 8 = 0
+      for (int x = 0; x < RX; ++x) {
+        const uint32_t tok = (s.first + i) * NK + r0 + 32 * x, kt = tok / kTileTok;
+        w.in[x] = pg[x] >= 0 && uint32_t(pg[x]) < a.c.num_pages;
+        if (pg[x] != -1 && !w.in[x] && a.status) set_status(a.status, KVC_ERR_CORRUPT);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) mk[x][g] = mv[x][g] = 0;
-        if (src) {
+        for (int q = 0; q < W; ++q) w.k[x][q] = w.v[x][q] = 0x88888888u;  // n - 8 = 0
+#pragma unroll
+        for (int g = 0; g < NG; ++g) w.mk[x][g] = w.mv[x][g] = 0;
+        if (w.in[x]) {
+          const uint8_t *src = base + int64_t(pg[x]) * a.c.s_p +
+                               int64_t(kt - fdiv(a.tpp, kt) * a.tpp.d) * C::TB;
+          const uint32_t ln = tok % kTileTok;
           const uint8_t *kr = src + ln * C::CB + 4 * W * p, *vr = kr + a.c.s_kv;
           if constexpr (W == 4) {
             const uint4 u = __ldg(reinterpret_cast<const uint4 *>(kr));
             const uint4 y = __ldg(reinterpret_cast<const uint4 *>(vr));
-            k[x][0] = u.x, k[x][1] = u.y, k[x][2] = u.z, k[x][3] = u.w;
-            v[x][0] = y.x, v[x][1] = y.y, v[x][2] = y.z, v[x][3] = y.w;
+            w.k[x][0] = u.x, w.k[x][1] = u.y, w.k[x][2] = u.z, w.k[x][3] = u.w;
+            w.v[x][0] = y.x, w.v[x][1] = y.y, w.v[x][2] = y.z, w.v[x][3] = y.w;
           } else {
             const uint2 u = __ldg(reinterpret_cast<const uint2 *>(kr));
             const uint2 y = __ldg(reinterpret_cast<const uint2 *>(vr));
-            k[x][0] = u.x, k[x][1] = u.y;
-            v[x][0] = y.x, v[x][1] = y.y;
+            w.k[x][0] = u.x, w.k[x][1] = u.y;
+            w.v[x][0] = y.x, w.v[x][1] = y.y;
           }
-          const uint32_t *m = reinterpret_cast<const uint32_t *>(src + kTileTok * C::CB) + ln * NG;
-          const uint32_t *n = reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(m) + a.c.s_kv);
+          const uint8_t *m = src + kTileTok * C::CB + ln * NG * 4;
 #pragma unroll
-          for (int g = 0; g < NG; ++g) mk[x][g] = __ldg(m + g), mv[x][g] = __ldg(n + g);
+          for (int g = 0; g < NG; ++g) {
+            w.mk[x][g] = __ldg(reinterpret_cast<const uint32_t *>(m) + g);
+            w.mv[x][g] = __ldg(reinterpret_cast<const uint32_t *>(m + a.c.s_kv) + g);
+          }
         }
       }
+      look(i + 2);
     };
-    if (s.tiles) load(s.first);
-    for (uint32_t i = 0; i < s.tiles; ++i, ++j) {
-      const uint32_t buf = j & 1;
-      if (j >= 2) pf_wait(pv + buf, ((j >> 1) - 1) & 1u, dead, a.status);
+    auto unpack = [&](const Raw &w, uint32_t j) {
+      const uint32_t buf = j % kPfStages, turn = j / kPfStages;
+      if (turn) pf_wait(pv + buf, (turn - 1) & 1u, dead, a.status);
       uint8_t *kb = smem + C::k + buf * C::KBUF, *vb = smem + C::v + buf * C::KBUF;
       float *meta = reinterpret_cast<float *>(smem + C::meta) + buf * C::MW * NK;
       uint32_t most = 0;
@@ -318,54 +355,57 @@ __device__ __forceinline__ void pf_unpack(const CacheAttnArgs &a, uint8_t *smem,
         uint8_t *kr = kb + row * 128, *vr = vb + row * 128;
 #pragma unroll
         for (int b = 0; b < W; ++b) {
-          const uint32_t w = k[x][b];
+          const uint32_t u = w.k[x][b];
           *reinterpret_cast<uint4 *>(kr + (b >> 1) * NK * 128 + (((4 * (b & 1) + p) ^ sw) << 4)) =
-              make_uint4(centred<false>(w), centred<true>(w), centred<false>(w >> 8),
-                         centred<true>(w >> 8));
+              make_uint4(centred<false>(u), centred<true>(u), centred<false>(u >> 8),
+                         centred<true>(u >> 8));
         }
         // values x 2^-e, e from the largest |z + 8 s| + 8 |s|
         bool bad = false;
         float bound = 0.f;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          bad |= not_finite(mv[x][g]);
-          bound = fmaxf(bound, fabsf(zero8(mv[x][g])) + 8.f * fabsf(half_lo(mv[x][g])));
+          bad |= not_finite(w.mv[x][g]);
+          bound = fmaxf(bound, fabsf(zero8(w.mv[x][g])) + 8.f * fabsf(half_lo(w.mv[x][g])));
         }
         const uint32_t ex = (__float_as_uint(bound) >> 23) & 255u;
         const bool none = bad || bound == 0.f;
         const float scale = none ? 1.f : __uint_as_float(ex << 23);
         const float inv = none ? (bad ? 0.f : 1.f) : __uint_as_float((254u - ex) << 23);
+        float sv[NG], zv[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const uint32_t m = bad ? 0u : w.mv[x][g];
+          sv[g] = half_lo(m) * inv;
+          zv[g] = zero8(m) * inv;
+        }
 #pragma unroll
         for (int q = 0; q < W; ++q) {
-          constexpr int B = D / 32;
-          const int wj = B * int(p) + q;               // stored word: halves of blocks a, a + 1
-          const int ga = ((2 * q) % B) * 32 / G, gb = ((2 * q) % B + 1) * 32 / G;
-          const uint32_t ma = bad ? 0u : mv[x][ga], mb = bad ? 0u : mv[x][gb];
-          const uint32_t s2 = f16x2(half_lo(ma) * inv, half_lo(mb) * inv);
-          const uint32_t z2 = f16x2(zero8(ma) * inv, zero8(mb) * inv);
-          const uint32_t w = v[x][q];
+          const int wj = W * int(p) + q;  // stored word: halves of 32-channel blocks a, a + 1
+          const int ga = ((2 * q) % W) * 32 / G, gb = ((2 * q) % W + 1) * 32 / G;
+          const uint32_t s2 = f16x2(sv[ga], sv[gb]), z2 = f16x2(zv[ga], zv[gb]), u = w.v[x][q];
           auto deq = [&](uint32_t n) {
             uint32_t d;
             asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(n), "r"(s2), "r"(z2));
             return d;
           };
           *reinterpret_cast<uint4 *>(vr + (wj >> 3) * NK * 128 + (((wj & 7) ^ sw) << 4)) =
-              make_uint4(deq(centred<false>(w)), deq(centred<true>(w)), deq(centred<false>(w >> 8)),
-                         deq(centred<true>(w >> 8)));
+              make_uint4(deq(centred<false>(u)), deq(centred<true>(u)), deq(centred<false>(u >> 8)),
+                         deq(centred<true>(u >> 8)));
         }
         if (int(p) < NG) {
-          uint32_t m = mk[x][0];
+          uint32_t m = w.mk[x][0];
 #pragma unroll
-          for (int g = 1; g < NG; ++g) m = int(p) == g ? mk[x][g] : m;
+          for (int g = 1; g < NG; ++g) m = int(p) == g ? w.mk[x][g] : m;
           meta[p * NK + row] = half_lo(m);
           meta[(NG + p) * NK + row] = zero8(m);
         }
-        const float bias = !in[x] ? -INFINITY : bad ? __uint_as_float(0x7FFFFFFFu) : 0.f;
-        if (p == 0) {
+        const float bias = !w.in[x] ? -INFINITY : bad ? __uint_as_float(0x7FFFFFFFu) : 0.f;
+        if (p == 3) {
           meta[2 * NG * NK + row] = scale;
           meta[(2 * NG + 1) * NK + row] = bias;
         }
-        odd |= !in[x] || bad;
+        odd |= !w.in[x] || bad;
         most = max(most, none ? 0u : __float_as_uint(scale));
       }
       most = __reduce_max_sync(0xFFFFFFFFu, most);
@@ -377,8 +417,78 @@ __device__ __forceinline__ void pf_unpack(const CacheAttnArgs &a, uint8_t *smem,
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full + buf);
-      if (i + 1 < s.tiles) load(s.first + i + 1);
+    };
+    Raw raw;
+    look(i0);
+    load(raw, i0);
+    for (uint32_t i = i0; i < tiles; i += 2) {
+      unpack(raw, j0 + i);
+      load(raw, i + 2);  // (past the segment's end: nothing is read)
     }
+  }
+}
+
+// The issuing warp: every tile's products, in the order QK 0, QK 1, then PV i, QK i + 2.
+// The tensor cores take them one after the other: a tile's scores are ready after the
+// values of the tile two before, whose weights they replace.
+template <int D, int G>
+__device__ __forceinline__ void pf_issue(const CacheAttnArgs &a, uint8_t *smem, uint32_t tm,
+                                         uint64_t f, uint64_t f_end) {
+  using C = PfCfg<D, G>;
+  constexpr int NG = C::NG, NK = C::NK, SG = G / 16;  // (16-channel steps of a group)
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::bars), *pv = full + kPfStages;
+  uint64_t *sready = pv + kPfStages, *pready = sready + 2, *qready = pready + 2;
+  volatile uint32_t *dead = reinterpret_cast<uint32_t *>(smem + C::ctl) + 1;
+  const uint32_t q_s = smem_u32(smem + C::q), k_s = smem_u32(smem + C::k), v_s = smem_u32(smem + C::v);
+  auto scores = [&](uint32_t j) {
+    const uint32_t buf = tm_uniform(j % kPfStages), w = tm_uniform(j & 1);
+    pf_wait(full + buf, (j / kPfStages) & 1u, dead, a.status);
+    tm_fence_after();
+    __syncwarp();
+    const uint64_t dq = tm_desc(q_s, 16, 1024), dk = tm_desc(k_s + buf * C::KBUF, 16, 1024);
+    const uint32_t ts = tm + C::tS + w * 128;
+    if (tm_elect()) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int st = 0; st < 2 * SG; ++st) {  // hi parts, then lo
+          const int s = g * SG + st % SG, o = (s & 3) * 2;
+          tm_mma(ts + g * NK, dq + (((st / SG) * C::QPART + (s >> 2) * kPfRows * 128) >> 4) + o,
+                 dk + (((s >> 2) * NK * 128) >> 4) + o, tm_idesc(NK, false), st != 0);
+        }
+      tm_commit(sready + w);
+    }
+    __syncwarp();
+  };
+  uint32_t j0 = 0;
+  for (uint32_t seg = 0; f < f_end;) {
+    const PfSegment s = pf_segment_at(a, f_end, f);
+    if (s.tiles == 0) continue;
+    const uint32_t tiles = tm_uniform(s.tiles);
+    pf_wait(qready, seg & 1u, dead, a.status);
+    tm_fence_after();
+    __syncwarp();
+    scores(j0);
+    if (tiles > 1) scores(j0 + 1);
+    for (uint32_t i = 0; i < tiles; ++i) {
+      const uint32_t j = j0 + i, w = tm_uniform(j & 1), buf = tm_uniform(j % kPfStages);
+      pf_wait(pready + w, (j >> 1) & 1u, dead, a.status);
+      tm_fence_after();
+      __syncwarp();
+      const uint64_t dv = tm_desc(v_s + buf * C::KBUF, NK * 128, 1024);
+      const uint32_t ts = tm + C::tS + w * 128, to = tm + C::tO + w * 128;
+      if (tm_elect()) {
+#pragma unroll
+        for (int st = 0; st < NK / 16; ++st)
+          tm_mma_ts(to, ts + st * 8, dv + st * 128, tm_idesc(D, true), i > 1 || st != 0);
+        tm_commit(pv + buf);
+      }
+      __syncwarp();
+      if (i + 2 < tiles) scores(j + 2);
+    }
+    __syncwarp();
+    j0 += s.tiles;
+    ++seg;
   }
 }
 
@@ -386,10 +496,11 @@ template <int D, int G>
 __global__ void __launch_bounds__(kPfThreads, 1)
     cache_prefill_kernel(const __grid_constant__ CacheAttnArgs a, const int dtype) {
   using C = PfCfg<D, G>;
-  constexpr int NG = C::NG, NK = C::NK, W = C::W, KH = NK / 2;
+  constexpr int NG = C::NG, NK = C::NK, W = C::W;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::bars), *sready = full + 2, *pv = full + 4;
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::bars), *pv = full + kPfStages;
+  uint64_t *sready = pv + kPfStages, *pready = sready + 2, *qready = pready + 2;
   uint32_t *ctl = reinterpret_cast<uint32_t *>(smem + C::ctl);
   volatile uint32_t *dead = ctl + 1;
   if (warp == 0) {
@@ -400,11 +511,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   if (tid == 32) {
-    for (int i = 0; i < 2; ++i) {
+    for (uint32_t i = 0; i < kPfStages; ++i) {
       mbar_init(full + i, 4);
-      mbar_init(sready + i, 1);
       mbar_init(pv + i, 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sready + i, 1);
+      mbar_init(pready + i, 4);
+    }
+    mbar_init(qready, kPfSoft / 32);
     mbar_fence_init();
     *dead = 0;
   }
@@ -418,34 +533,20 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   uint64_t f = uint64_t(blockIdx.x) * share;
   const uint64_t f_end = min(total, f + share);
 
-  if (warp >= kPfSoft / 32) {
-    pf_unpack<D, G>(a, smem, f, f_end);
+  if (warp >= (kPfSoft + kPfUnpack) / 32) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPfIssueRegs));
+    if (warp == (kPfSoft + kPfUnpack) / 32) pf_issue<D, G>(a, smem, tm_uniform(tm), f, f_end);
+  } else if (warp >= kPfSoft / 32) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPfUnpackRegs));
+    pf_unpack<D, G>(a, smem, uint32_t(warp >> 2) & 1u, f, f_end);
   } else {
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPfSoftRegs));
+    const int which = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t tl = tm + (uint32_t((warp & 3) * 32) << 16);  // this warp's lanes
+    const uint32_t tO = tl + C::tO + which * 128;
     float *fcs = reinterpret_cast<float *>(smem + C::fc), *qss = reinterpret_cast<float *>(smem + C::qs);
-    float *mxs = reinterpret_cast<float *>(smem + C::mx);
-    const uint32_t q_s = smem_u32(smem + C::q);
-    uint32_t j = 0;  // tiles so far
-
-    auto scores = [&](uint32_t jj) {  // thread 0: S of tile jj
-      const uint32_t buf = jj & 1, k_s = smem_u32(smem + C::k) + buf * C::KBUF;
-      pf_wait(full + buf, (jj >> 1) & 1u, dead, a.status);
-      tm_fence_after();
-#pragma unroll
-      for (int g = 0; g < NG; ++g)
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int st = g * G / 16; st < (g + 1) * G / 16; ++st) {
-            const uint32_t o = (st & 3) * 32;
-            tm_mma(tm + C::tS + buf * 128 + g * NK,
-                   tm_desc(q_s + part * C::QPART + (st >> 2) * kPfRows * 128 + o, 16, 1024),
-                   tm_desc(k_s + (st >> 2) * NK * 128 + o, 16, 1024), tm_idesc(NK, false),
-                   part != 0 || st != g * G / 16);
-          }
-      tm_commit(sready + buf);
-    };
+    float2 *fin = reinterpret_cast<float2 *>(smem + C::fin);
+    uint32_t j0 = 0;  // tiles before the segment
 
     while (f < f_end) {
       const PfSegment s = pf_segment_at(a, f_end, f);
@@ -453,15 +554,30 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // ---- the block's queries: qt as hi and lo parts, factors, group sums
 #pragma unroll 2
       for (int q = 0; q < kPfRows / 8; ++q) {
-        const int rr = warp * (kPfRows / 8) + q;
-        const bool live = uint32_t(rr) < s.nc;
-        const uint32_t gr = s.c0 + (live ? rr : 0), qi = gr / a.qpk;
+        const int rr = q * 8 + warp;  // (few rows: each warp has some)
+        const int i = lane & 7, pos = i < 4 ? 2 * i : 2 * (i - 4) + 1;
+        uint8_t *dst = smem + C::q + rr * 128 + 2 * pos;
+        if (uint32_t(rr) >= s.nc) {  // rows that are not there: zeros
+          if (lane == 0) {
+            fcs[rr] = 8.f;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) qss[g * kPfRows + rr] = 0.f;
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int sl = 0; sl < C::SL; ++sl)
+              *reinterpret_cast<uint32_t *>(smem + C::q + x * C::QPART + sl * kPfRows * 128 +
+                                            rr * 128 + 4 * lane) = 0;
+          continue;
+        }
+        const uint32_t gr = s.c0 + rr, qi = gr / a.qpk;
         const uint8_t *src = a.q + int64_t(s.l) * a.q_l + int64_t(s.rs.q0 + qi) * a.q_t +
                              int64_t(s.h * a.qpk + (gr - qi * a.qpk)) * a.q_h;
         uint16_t in[W];
 #pragma unroll
         for (int c = 0; c < W; ++c)
-          in[c] = live ? __ldg(reinterpret_cast<const uint16_t *>(src) + lane + 32 * c) : uint16_t(0);
+          in[c] = __ldg(reinterpret_cast<const uint16_t *>(src) + lane + 32 * c);
         uint64_t w0 = a.c.w0, w1 = a.c.w1;
         if (a.c.vec_signs) {
           uint64_t st = a.c.seed + (uint64_t(s.l) * 2 * a.c.heads + s.h) * uint64_t(D / 64) *
@@ -516,24 +632,20 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
           for (int g = 0; g < NG; ++g) qss[g * kPfRows + rr] = gs[g] * es;
         }
-        const int i = lane & 7, pos = i < 4 ? 2 * i : 2 * (i - 4) + 1;
 #pragma unroll
         for (int c = 0; c < W; ++c) {
           float vh, vl;
           split_f16(y[c] * es, vh, vl);
-          uint8_t *dst = smem + C::q + (c >> 1) * kPfRows * 128 + rr * 128 +
-                         (((4 * (c & 1) + (lane >> 3)) ^ (rr & 7)) << 4) + 2 * pos;
-          *reinterpret_cast<uint16_t *>(dst) = __half_as_ushort(__float2half_rn(vh));
-          *reinterpret_cast<uint16_t *>(dst + C::QPART) = __half_as_ushort(__float2half_rn(vl));
+          const uint32_t o = (c >> 1) * kPfRows * 128 + (((4 * (c & 1) + (lane >> 3)) ^ (rr & 7)) << 4);
+          *reinterpret_cast<uint16_t *>(dst + o) = __half_as_ushort(__float2half_rn(vh));
+          *reinterpret_cast<uint16_t *>(dst + o + C::QPART) = __half_as_ushort(__float2half_rn(vl));
         }
       }
       fence_proxy_async_smem();
-      tm_fence_before();  // (the output of the segment before is read)
-      named_bar_sync(1, kPfSoft);
-      if (tid == 0) {
-        scores(j);
-        if (s.tiles > 1) scores(j + 1);
-      }
+      tm_fence_before();  // (the segment before has been read)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qready);
+      named_bar_sync(1, kPfSoft);  // every row's factor and sums
       const float fc = fcs[row];
       float qsum[NG];
 #pragma unroll
@@ -544,53 +656,53 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // values' common exponent: weights times 2^(a value's e) reach up to 2^15).
       float nm = 0.f, mt = 0.f, thr = -INFINITY, l = 0.f, lw = 0.f, v_most = 0.f;
 
-      for (uint32_t i = 0; i < s.tiles; ++i, ++j) {
-        const uint32_t buf = j & 1;
+      for (uint32_t i = (which ^ j0) & 1u; i < s.tiles; i += 2) {
+        const uint32_t j = j0 + i, buf = j % kPfStages, tS = tl + C::tS + which * 128;
         const int32_t t0 = int32_t((s.first + i) * NK);
-        pf_wait(full + buf, (j >> 1) & 1u, dead, a.status);  // the keys' numbers
-        pf_wait(sready + buf, (j >> 1) & 1u, dead, a.status);
+        pf_wait(full + buf, (j / kPfStages) & 1u, dead, a.status);  // the keys' numbers
+        pf_wait(sready + which, (j >> 1) & 1u, dead, a.status);
         tm_fence_after();
         __syncwarp();
-        const float *meta = reinterpret_cast<const float *>(smem + C::meta) + buf * C::MW * NK + half * KH;
-        float sc[KH];
+        const float *meta = reinterpret_cast<const float *>(smem + C::meta) + buf * C::MW * NK;
+        float sc[NK];
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          float acc[KH];
+        for (int x0 = 0; x0 < NK; x0 += 16) {
+          float acc[NG][16];
 #pragma unroll
-          for (int x = 0; x < KH; x += 16)
-            tm_ld16(tl + C::tS + buf * 128 + g * NK + half * KH + x, acc + x);
+          for (int g = 0; g < NG; ++g) tm_ld16(tS + g * NK + x0, acc[g]);
           tm_wait_ld();
 #pragma unroll
-          for (int x = 0; x < KH; x += 16) tm_loaded16(acc + x);
-          const float2 q2 = make_float2(qsum[g], qsum[g]);
+          for (int g = 0; g < NG; ++g) tm_loaded16(acc[g]);
 #pragma unroll
-          for (int x = 0; x < KH; x += 4) {
-            const float4 ks = *reinterpret_cast<const float4 *>(meta + g * NK + x);
-            const float4 kz = *reinterpret_cast<const float4 *>(meta + (NG + g) * NK + x);
-            float2 u = g == 0 ? mul2(make_float2(kz.x, kz.y), q2)
-                              : fma2(make_float2(kz.x, kz.y), q2, make_float2(sc[x], sc[x + 1]));
-            float2 v = g == 0 ? mul2(make_float2(kz.z, kz.w), q2)
-                              : fma2(make_float2(kz.z, kz.w), q2, make_float2(sc[x + 2], sc[x + 3]));
-            u = fma2(make_float2(ks.x, ks.y), make_float2(acc[x], acc[x + 1]), u);
-            v = fma2(make_float2(ks.z, ks.w), make_float2(acc[x + 2], acc[x + 3]), v);
-            sc[x] = u.x, sc[x + 1] = u.y, sc[x + 2] = v.x, sc[x + 3] = v.y;
+          for (int g = 0; g < NG; ++g) {
+            const float2 q2 = make_float2(qsum[g], qsum[g]);
+#pragma unroll
+            for (int y = 0; y < 16; y += 4) {
+              const int x = x0 + y;
+              const float4 ks = *reinterpret_cast<const float4 *>(meta + g * NK + x);
+              const float4 kz = *reinterpret_cast<const float4 *>(meta + (NG + g) * NK + x);
+              float2 u = g == 0 ? mul2(make_float2(kz.x, kz.y), q2)
+                                : fma2(make_float2(kz.x, kz.y), q2, make_float2(sc[x], sc[x + 1]));
+              float2 v = g == 0 ? mul2(make_float2(kz.z, kz.w), q2)
+                                : fma2(make_float2(kz.z, kz.w), q2, make_float2(sc[x + 2], sc[x + 3]));
+              u = fma2(make_float2(ks.x, ks.y), make_float2(acc[g][y], acc[g][y + 1]), u);
+              v = fma2(make_float2(ks.z, ks.w), make_float2(acc[g][y + 2], acc[g][y + 3]), v);
+              sc[x] = u.x, sc[x + 1] = u.y, sc[x + 2] = v.x, sc[x + 3] = v.y;
+            }
           }
         }
         const uint4 odd = *reinterpret_cast<const uint4 *>(smem + C::wodd + buf * 16);
         if ((odd.x | odd.y | odd.z | odd.w) || t0 < s.all_lo || t0 + NK > s.all_hi) {
 #pragma unroll
-          for (int x = 0; x < KH; ++x) {
-            const int32_t t = t0 + half * KH + x;
+          for (int x = 0; x < NK; ++x) {
+            const int32_t t = t0 + x;
             sc[x] = t >= lo && t < hi ? sc[x] + meta[(2 * NG + 1) * NK + x] : -INFINITY;
           }
         }
-        float top = sc[0];
+        float tops[4] = {sc[0], sc[1], sc[2], sc[3]};
 #pragma unroll
-        for (int x = 1; x < KH; ++x) top = fmaxf(top, sc[x]);
-        float *mx = mxs + buf * 2 * kPfRows;
-        mx[half * kPfRows + row] = top;
-        named_bar_sync(1, kPfSoft);
-        top = fmaxf(top, mx[(1 - half) * kPfRows + row]);
+        for (int x = 4; x < NK; ++x) tops[x & 3] = fmaxf(tops[x & 3], sc[x]);
+        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         const float4 wm = *reinterpret_cast<const float4 *>(smem + C::wmax + buf * 16);
         const float vm = fmaxf(fmaxf(wm.x, wm.y), fmaxf(wm.z, wm.w));
         if (__any_sync(0xFFFFFFFFu, top > thr) || vm > v_most) {
@@ -612,29 +724,24 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           }
           nm = lw - mt;
           l *= fac;
-          if (i > 0) {
-            const uint32_t jp = j - 1;
-            pf_wait(pv + (jp & 1), (jp >> 1) & 1u, dead, a.status);
-            tm_fence_after();
-            __syncwarp();
+          if (i > 1) {  // (the values of this softmax's last tile are in: its scores came after)
 #pragma unroll
-            for (int x = 0; x < D / 2; x += 16) {
+            for (int x = 0; x < D; x += 16) {
               float o[16];
-              tm_ld16(tl + C::tO + half * (D / 2) + x, o);
+              tm_ld16(tO + x, o);
               tm_wait_ld();
               tm_loaded16(o);
 #pragma unroll
               for (int y = 0; y < 16; ++y) o[y] *= fac;
-              tm_st16(tl + C::tO + half * (D / 2) + x, o);
+              tm_st16(tO + x, o);
             }
-            tm_wait_st();
           }
         }
         const float *vs = meta + 2 * NG * NK;
         const float2 f2 = make_float2(fc, fc), n2 = make_float2(nm, nm);
-        float2 l2 = make_float2(0.f, 0.f);
+        float2 l2 = make_float2(0.f, 0.f), l3 = l2;
 #pragma unroll
-        for (int x = 0; x < KH; x += 16) {
+        for (int x = 0; x < NK; x += 16) {
           uint32_t pk[8];
 #pragma unroll
           for (int y = 0; y < 16; y += 4) {
@@ -642,63 +749,64 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const float2 u = fma2(make_float2(sc[x + y], sc[x + y + 1]), f2, n2);
             const float2 v = fma2(make_float2(sc[x + y + 2], sc[x + y + 3]), f2, n2);
             const float2 pu = make_float2(ex2(u.x), ex2(u.y)), pw = make_float2(ex2(v.x), ex2(v.y));
-            l2 = add2(l2, add2(pu, pw));
+            l2 = add2(l2, pu);
+            l3 = add2(l3, pw);
             const float2 wu = mul2(pu, make_float2(sv.x, sv.y)), ww = mul2(pw, make_float2(sv.z, sv.w));
             pk[y / 2] = f16x2(wu.x, wu.y);
             pk[y / 2 + 1] = f16x2(ww.x, ww.y);
           }
-          tm_st8(tl + C::tP + buf * 64 + half * (KH / 2) + x / 2, pk);
+          tm_st8(tS + x / 2, pk);
         }
+        l2 = add2(l2, l3);
         l += l2.x + l2.y;
         tm_wait_st();
         tm_fence_before();
-        named_bar_sync(2, kPfSoft);
-        if (tid == 0) {
-          tm_fence_after();
-          const uint32_t v_s = smem_u32(smem + C::v) + buf * C::KBUF;
-#pragma unroll
-          for (int st = 0; st < NK / 16; ++st)
-            tm_mma_ts(tm + C::tO, tm + C::tP + buf * 64 + st * 8,
-                      tm_desc(v_s + st * 2048, NK * 128, 1024), tm_idesc(D, true), i != 0 || st != 0);
-          tm_commit(pv + buf);
-          if (i + 2 < s.tiles) scores(j + 2);
-        }
         __syncwarp();
+        if (lane == 0) mbar_arrive(pready + which);
       }
 
-      // ---- the segment's record
-      pf_wait(pv + ((j - 1) & 1), ((j - 1) >> 1) & 1u, dead, a.status);
+      // ---- the segment's record, of both softmaxes' results
+      j0 += s.tiles;
+      pf_wait(pv + (j0 - 1) % kPfStages, ((j0 - 1) / kPfStages) & 1u, dead, a.status);
       tm_fence_after();
-      __syncwarp();
-      float *lx = mxs + half * kPfRows;  // (the last tile's maxima are read: barrier 2)
-      lx[row] = l;
+      fin[which * kPfRows + row] = make_float2(thr == -INFINITY ? -INFINITY : mt - lw, l);
       named_bar_sync(1, kPfSoft);
+      const float2 mine[2] = {fin[row], fin[kPfRows + row]};
+      const float m = fmaxf(mine[0].x, mine[1].x);
+      float w[2];
+      bool has[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {  // (a maximum of -inf: zeros, or NaN, which stay)
+        has[x] = s.tiles > 1 || ((j0 - 1) & 1u) == uint32_t(x);
+        w[x] = mine[x].x == -INFINITY ? 1.f : ex2(mine[x].x - m);
+      }
       float *rec = a.rec + (s.unit + blockIdx.x) * uint64_t(kPfRows * (4 + D)) + row * (4 + D);
       const bool live = uint32_t(row) < s.nc;
-      if (live && half == 0)
-        *reinterpret_cast<float2 *>(rec) =
-            make_float2(thr == -INFINITY ? -INFINITY : mt - lw, mxs[row] + mxs[kPfRows + row]);
+      if (live && which == 0)
+        *reinterpret_cast<float2 *>(rec) = make_float2(m, mine[0].y * w[0] + mine[1].y * w[1]);
 #pragma unroll
-      for (int x = 0; x < D / 2; x += 16) {
-        float o[16];
-        tm_ld16(tl + C::tO + half * (D / 2) + x, o);
+      for (int x = 0; x < D / 2; x += 16) {  // half of the columns each
+        float o[16], o1[16];
+        tm_ld16(tl + C::tO + which * (D / 2) + x, o);
+        tm_ld16(tl + C::tO + 128 + which * (D / 2) + x, o1);
         tm_wait_ld();
         tm_loaded16(o);
+        tm_loaded16(o1);
+#pragma unroll
+        for (int y = 0; y < 16; ++y)
+          o[y] = 8.f * ((has[0] ? o[y] * w[0] : 0.f) + (has[1] ? o1[y] * w[1] : 0.f));
 #pragma unroll
         for (int y = 0; y < 16; y += 8) {
           // columns of stored word wj: halves of its two 32-channel blocks
-          const int wj = (half * (D / 2) + x + y) / 8, hs = 2 * wj;
+          const int wj = (which * (D / 2) + x + y) / 8, hs = 2 * wj;
           const int ch = 32 * (hs % W) + 4 * (hs / W);
           if (live) {
-            *reinterpret_cast<float4 *>(rec + 4 + ch) =
-                make_float4(8.f * o[y], 8.f * o[y + 2], 8.f * o[y + 4], 8.f * o[y + 6]);
+            *reinterpret_cast<float4 *>(rec + 4 + ch) = make_float4(o[y], o[y + 2], o[y + 4], o[y + 6]);
             *reinterpret_cast<float4 *>(rec + 4 + ch + 32) =
-                make_float4(8.f * o[y + 1], 8.f * o[y + 3], 8.f * o[y + 5], 8.f * o[y + 7]);
+                make_float4(o[y + 1], o[y + 3], o[y + 5], o[y + 7]);
           }
         }
       }
-      tm_fence_before();
-      named_bar_sync(2, kPfSoft);  // the shared arrays are free for the next segment
     }
   }
   tm_fence_before();

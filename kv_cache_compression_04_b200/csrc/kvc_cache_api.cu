@@ -129,10 +129,10 @@ kvc_status load_shape(const kvc_cache_desc *c, const int32_t *seq_lens, int32_t 
   return KVC_OK;
 }
 
-// The attention's workspace: prefixes of work and the requests' shapes; up to 16 rows per
-// request, query fragments per unit (layer, kv head, request); more, the blocks of 128
-// rows; then one record per unit (a block's, with more than 16 rows) and per warp or CTA
-// (each cols x (4 + head_dim) fp32).
+// The attention's workspace: prefixes of work and the requests' shapes; query fragments
+// per unit (layer, kv head, block of up to 16 rows of a request), or the numbers of the
+// blocks of 128 rows; then one record per unit and per warp or CTA (each cols x (4 +
+// head_dim) fp32).
 struct AttnWs {
   uint64_t blocks = 0, shapes = 0, frags = 0, rec = 0, total = 0;
 };
@@ -152,12 +152,12 @@ kvc_status check_attn(const kvc_cache_desc *cache, const kvc_cache_attn *t, Cach
   const uint64_t heads = uint64_t(cache->kv_heads), qpk = uint64_t(t->q_per_kv);
   const uint64_t rows = uint64_t(t->max_q) * qpk, cols = uint64_t(cache_cols(rows));
   const uint64_t reqs = uint64_t(t->n_requests), lh = uint64_t(cache->layers) * heads;
-  w.blocks = cols > 16 ? uint64_t(t->q_tokens) * qpk / cols + reqs : reqs;
+  w.blocks = cols > 16 ? uint64_t(t->q_tokens) * qpk / cols + reqs : reqs * ((rows + cols - 1) / cols);
   const uint64_t units = lh * w.blocks;
   // (query rows of a request, and units, are counted in 32 bits)
   if (units >= (uint64_t(1) << 31) - 1 || uint64_t(t->q_tokens) * qpk >= (uint64_t(1) << 31))
     return KVC_ERR_UNSUPPORTED;
-  w.shapes = round256(8 * (w.blocks + 1));
+  w.shapes = round256(8 * ((cols > 16 ? w.blocks : reqs) + 1));
   w.frags = w.shapes + round256(16 * reqs);
   const uint64_t frags = cols > 16 ? 16 * w.blocks : units * cache_frag_bytes(cache->head_dim, int(cols));
   w.rec = round256(w.frags + frags);
@@ -300,6 +300,7 @@ kvc_status kvc_cache_attend(const kvc_cache_desc *cache, const kvc_cache_attn *t
   const uint64_t reach = uint64_t(t->page_table_stride) * p.pt.d;
   a.max_len = uint32_t(reach < 0x7FFFFFFFull ? reach : 0x7FFFFFFFull);
   a.max_blocks = uint32_t(w.blocks);
+  a.row_blocks = uint32_t(w.blocks / uint64_t(t->n_requests));
   a.tpp = make_fastdiv(p.pt.d / kTileTok);
   a.q = static_cast<const uint8_t *>(t->q);
   a.q_l = t->q_stride_layer * 2;
@@ -320,7 +321,7 @@ kvc_status kvc_cache_attend(const kvc_cache_desc *cache, const kvc_cache_attn *t
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const int g = cache->group_size;
   cudaError_t e;
-  if (uint64_t(t->max_q) * uint64_t(t->q_per_kv) > 16)
+  if (uint64_t(t->max_q) * uint64_t(t->q_per_kv) > kCacheFewRows)
     e = cache->head_dim == 128 ? launch_cache_prefill_d128(g, t->dtype, a, sms, cs)
                                : launch_cache_prefill_d64(g, t->dtype, a, sms, cs);
   else

@@ -28,11 +28,11 @@
 // output to fp16). Up to 4 rows, columns 2 i, 2 i + 1 are row i's two parts in both
 // products.
 //
-// Up to 16 query rows (queries x query heads per kv head) of a request; more are
-// kvc_cache_prefill.cuh's.
+// Few query rows (queries x query heads per kv head) of a request, 16 at a time; many are
+// kvc_cache_prefill.cuh's (kCacheFewRows).
 //
-// Work. A unit is (layer, kv head, request); its keys are chunks of 32 tokens (two
-// tiles). All units' chunks in a row, each unit with
+// Work. A unit is (layer, kv head, block of a request's rows); its keys are chunks of 32
+// tokens (two tiles). All units' chunks in a row, each unit with
 // kCaLead chunks' worth of fixed work before them, are cut in equal shares, one per
 // warp, from the lengths on the device: ragged batches and single long requests
 // balance alike, and a captured call follows its lengths. A warp's part of a unit is
@@ -79,9 +79,15 @@ __device__ __forceinline__ KeyChunks key_chunks(const CacheAttnArgs &a, const Re
   const uint32_t first = lo > 0 ? uint32_t(lo) / kChunkTok : 0;
   return KeyChunks{first, (s.len + kChunkTok - 1) / kChunkTok - first};
 }
-// A unit's work: its chunks, and kCaLead before them; none without chunks.
+// A unit's work: the chunks of its request's keys, and kCaLead before them; none without
+// chunks.
 __device__ __forceinline__ uint32_t unit_work(const KeyChunks &k) {
   return k.count ? k.count + kCaLead : 0;
+}
+// A request's blocks of query rows.
+template <int COLS>
+__device__ __forceinline__ uint32_t row_blocks(const CacheAttnArgs &a, const ReqShape &s) {
+  return (s.nq * a.qpk + COLS - 1) / COLS;
 }
 // Warp g (of all CTAs) takes the work [g * share, (g + 1) * share) of all units'
 // in a row.
@@ -140,7 +146,7 @@ __global__ void __launch_bounds__(kCaPrepWarps * 32)
       const ReqShape s = read_request(a, r, ok);
       bad |= !ok;
       a.shapes[r] = make_uint4(s.nq, s.q0, s.len, 0);
-      w += unit_work(key_chunks(a, s));
+      w += uint64_t(unit_work(key_chunks(a, s))) * row_blocks<COLS>(a, s);
     }
     if (bad && a.status) set_status(a.status, KVC_ERR_CORRUPT);
     uint64_t wi = w;
@@ -156,21 +162,22 @@ __global__ void __launch_bounds__(kCaPrepWarps * 32)
     for (uint32_t r = r0; r < r1; ++r) {
       a.wpre[r] = base;
       const uint4 v = a.shapes[r];
-      base += unit_work(key_chunks(a, ReqShape{v.x, v.y, v.z}));
+      const ReqShape s{v.x, v.y, v.z};
+      base += uint64_t(unit_work(key_chunks(a, s))) * row_blocks<COLS>(a, s);
     }
     if (tid == T - 1) a.wpre[n] = base;
     return;
   }
-  const uint32_t unit = blockIdx.x - 1, lh = unit / n, r = unit - lh * n;
-  const uint32_t l = lh / H, h = lh - l * H;
+  const uint32_t unit = blockIdx.x - 1, lr = unit / a.row_blocks, lh = lr / n, r = lr - lh * n;
+  const uint32_t l = lh / H, h = lh - l * H, c0 = (unit - lr * a.row_blocks) * COLS;
   bool ok;
   const ReqShape rs = read_request(a, r, ok);
-  if (!ok || key_chunks(a, rs).count == 0) return;
   const uint32_t rows = rs.nq * a.qpk;
+  if (!ok || c0 >= rows || key_chunks(a, rs).count == 0) return;
   __shared__ alignas(16) uint8_t frag[C::QB];
   for (int col = warp; col < COLS; col += kCaPrepWarps) {
-    const bool live = uint32_t(col) < rows;
-    const uint32_t row = live ? col : 0, qi = row / a.qpk;
+    const bool live = c0 + col < rows;
+    const uint32_t row = live ? c0 + col : 0, qi = row / a.qpk;
     const uint8_t *src = a.q + int64_t(l) * a.q_l + int64_t(rs.q0 + qi) * a.q_t +
                          int64_t(h * a.qpk + (row - qi * a.qpk)) * a.q_h;
     uint16_t in[C::W];
@@ -262,7 +269,7 @@ __global__ void __launch_bounds__(kCaPrepWarps * 32)
 
 // A warp's part of a unit.
 struct Segment {
-  uint32_t l, h, r, nc;          // layer, kv head, request; its query rows
+  uint32_t l, h, r, c0, nc;      // layer, kv head, request; first query row, rows
   uint32_t first, chunks;        // the segment's chunks
   uint64_t unit, u0, u1;         // the unit, and its work [u0, u1)
   int32_t any_lo, any_hi, all_lo, all_hi;  // keys that some row sees, that every row sees
@@ -270,6 +277,7 @@ struct Segment {
 };
 // The segment at f, the place of the next one (as f). chunks may be 0: the share
 // ends inside a unit's fixed work.
+template <int COLS>
 __device__ __forceinline__ Segment segment_at(const CacheAttnArgs &a, const uint64_t *wpre,
                                               uint64_t f_end, uint64_t &f) {
   const uint32_t n = a.n_req;
@@ -282,9 +290,11 @@ __device__ __forceinline__ Segment segment_at(const CacheAttnArgs &a, const uint
   s.rs = request_shape(a, lo);
   const KeyChunks kc = key_chunks(a, s.rs);
   const uint32_t work = unit_work(kc);
-  s.nc = s.rs.nq * a.qpk;
-  s.unit = lh * n + lo;
-  const uint32_t at = uint32_t(in_lh - wpre[lo]);
+  const uint64_t in_r = in_lh - wpre[lo];
+  const uint32_t block = uint32_t(div64(in_r, work)), at = uint32_t(in_r - uint64_t(block) * work);
+  s.c0 = block * COLS;
+  s.nc = min(uint32_t(COLS), s.rs.nq * a.qpk - s.c0);
+  s.unit = (lh * n + lo) * a.row_blocks + block;
   const uint32_t end = uint32_t(min(uint64_t(work), at + (f_end - f)));
   const uint32_t c_at = at > kCaLead ? at - kCaLead : 0, c_end = end > kCaLead ? end - kCaLead : 0;
   s.first = kc.first + c_at;
@@ -293,8 +303,8 @@ __device__ __forceinline__ Segment segment_at(const CacheAttnArgs &a, const uint
   s.u1 = s.u0 + work;
   f += end - at;
   // rows are ordered by query
-  key_range(a, s.rs, 0, s.any_lo, s.all_hi);
-  key_range(a, s.rs, s.rs.nq - 1, s.all_lo, s.any_hi);
+  key_range(a, s.rs, s.c0 / a.qpk, s.any_lo, s.all_hi);
+  key_range(a, s.rs, (s.c0 + s.nc - 1) / a.qpk, s.all_lo, s.any_hi);
   return s;
 }
 
@@ -336,7 +346,7 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
     // a warp with nothing to do still looks whether it is to take part in a merge
     const bool idle = f >= f_end;
     uint64_t next = idle ? cta1 - 1 : f;
-    Segment s = segment_at(a, wpre, idle ? cta1 : f_end, next);
+    Segment s = segment_at<COLS>(a, wpre, idle ? cta1 : f_end, next);
     if (idle) s.chunks = 0;
     f = next;
     // The CTA's whole share in one unit: its warps are merged to one record.
@@ -516,7 +526,7 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
 #pragma unroll
           for (int i = 0; i < R; ++i) {
             lim[i] = make_int2(0, 0);
-            if (uint32_t(row_of(i)) < s.nc) key_range(a, s.rs, row_of(i) / a.qpk, lim[i].x, lim[i].y);
+            if (uint32_t(row_of(i)) < s.nc) key_range(a, s.rs, (s.c0 + row_of(i)) / a.qpk, lim[i].x, lim[i].y);
           }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
@@ -762,10 +772,11 @@ struct DecodeRecords {
     const uint64_t lh = uint64_t(l) * H + h, per_lh = a.wpre[n], total = per_lh * H * a.c.layers;
     const uint64_t share = work_per_warp(total, grid * CW), cta = share * CW;
     // the unit's work [u0, u1), its chunks from u0 + kCaLead; the warps that have them
-    const uint64_t u0 = lh * per_lh + a.wpre[r], u1 = u0 + work;
+    const uint32_t block = row_ / COLS;
+    const uint64_t u0 = lh * per_lh + a.wpre[r] + uint64_t(block) * work, u1 = u0 + work;
     const uint32_t g0 = uint32_t(div64(u0 + kCaLead, share)), g1 = uint32_t(div64(u1 - 1, share));
-    unit = lh * n + r;
-    row = row_;
+    unit = (lh * n + r) * a.row_blocks + block;
+    row = row_ - block * COLS;
     b0 = g0 / CW;
     b1 = g1 / CW;
     const bool m0 = uint64_t(b0) * cta >= u0 && min(total, (uint64_t(b0) + 1) * cta) <= u1;
@@ -797,7 +808,7 @@ cudaError_t cache_attend_t(int dtype, const CacheAttnArgs &a, int sms, cudaStrea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.stream = st;
-  const uint64_t units = uint64_t(a.c.layers) * a.c.heads * a.n_req;
+  const uint64_t units = uint64_t(a.c.layers) * a.c.heads * a.n_req * a.row_blocks;
   cache_attend_prep_kernel<D, G, NB><<<unsigned(units + 1), kCaPrepWarps * 32, 0, st>>>(a, dtype);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

@@ -451,8 +451,9 @@ typedef struct {
  * named twice holds a mixture of its rows. A vector that transforms to inf or
  * NaN (KVC_ERR_NONFINITE), or whose scale or zero overflows fp16
  * (KVC_ERR_RANGE), is stored with NaN scales, so that whatever reads it gives
- * NaN; other rows are not affected. A slot outside the pool sets
- * KVC_ERR_CORRUPT and its token is skipped. One kernel. */
+ * NaN (codes 0); other rows are not affected. A slot outside the pool sets
+ * KVC_ERR_CORRUPT and its token is skipped. One kernel, in a form for few rows
+ * or for many, whose results are the same. */
 kvc_status kvc_cache_write(const kvc_cache_desc *cache, const kvc_cache_rows *rows,
                            uint32_t *status, kvc_stream_t stream);
 
@@ -460,7 +461,7 @@ kvc_status kvc_cache_write(const kvc_cache_desc *cache, const kvc_cache_rows *ro
  * dtype, into rows->k and rows->v. Values past fp16's range become infinite.
  * Rows with a negative slot are left as they were; a slot outside the pool
  * sets KVC_ERR_CORRUPT and its rows are left as they were. Slots may repeat.
- * One kernel. */
+ * One kernel, in a form for few rows or for many, whose results are the same. */
 kvc_status kvc_cache_read(const kvc_cache_desc *cache, const kvc_cache_rows *rows,
                           uint32_t *status, kvc_stream_t stream);
 
@@ -468,8 +469,8 @@ kvc_status kvc_cache_read(const kvc_cache_desc *cache, const kvc_cache_rows *row
  * vectors of the stream's token t (requests concatenated in order, as
  * kvc_compress codes them) go to slots[t] (DEVICE, [sum of seq_lens]; negative:
  * the token is skipped). The stream must describe layers x kv_heads x
- * head_dim vectors of these requests, 4-bit ASYM or SYM codes of this group
- * size, the same sign mode and the same diagonals (with per-vector diagonals
+ * head_dim vectors of as many requests and tokens, 4-bit ASYM or SYM codes of
+ * this group size, the same sign mode and the same diagonals (with per-vector diagonals
  * and first_layer > 0: a stream of those layers alone whose seed is the one
  * whose diagonal 0 is theirs, see kvc_cache_stream_seed), and store its code
  * chunks raw, as kvc_attend asks; else KVC_ERR_CORRUPT, and the slots' content
@@ -503,7 +504,10 @@ uint64_t kvc_cache_stream_seed(const kvc_cache_desc *cache);
  * never used. A request whose q_starts or seq_lens is out of range (decreasing
  * or outside [0, q_tokens]; more than max_q queries; a length below 0 or past
  * its row of the page table) sets KVC_ERR_CORRUPT and its rows are left as they
- * were; a page outside the pool sets it too and the page's tokens are left out. */
+ * were (where q_starts decrease, the other requests' rows are unspecified); a
+ * page outside the pool sets it too and the page's tokens are left out.
+ * Three kernels. max_q and q_per_kv choose the form: up to 48 query rows
+ * (max_q * q_per_kv) are taken 4, 8 or 16 at a time, more in blocks of 128. */
 #define KVC_CACHE_MAX_Q_PER_KV 64
 typedef struct {
   int32_t dtype;              /* KVC_BF16 or KVC_FP16, of q and out */
@@ -517,8 +521,9 @@ typedef struct {
   int64_t q_tokens;           /* rows of q, 0 .. 2^24 */
   const int32_t *q_starts;    /* DEVICE [n_requests + 1], or null */
   const int32_t *seq_lens;    /* DEVICE [n_requests] */
-  const int32_t *page_table;  /* DEVICE [n_requests][page_table_stride] */
-  int64_t page_table_stride;
+  const int32_t *page_table;  /* DEVICE [n_requests][page_table_pages] */
+  int64_t page_table_pages;   /* a request's entries, >= 0 */
+  int64_t page_table_stride;  /* elements between requests, >= 0 */
   const void *q;              /* DEVICE [layers][q_tokens][kv_heads * q_per_kv][head_dim] */
   int64_t q_stride_layer, q_stride_token, q_stride_head;  /* elements, multiples of 8 */
   void *out;                  /* DEVICE, as q */

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libkvc.so")
@@ -94,7 +95,8 @@ class kvc_cache_attn(C.Structure):
                 ("max_q", C.c_int32), ("causal", C.c_int32), ("window", C.c_int32),
                 ("scale", C.c_float), ("reserved", C.c_int32), ("q_tokens", C.c_int64),
                 ("q_starts", C.c_void_p), ("seq_lens", C.c_void_p), ("page_table", C.c_void_p),
-                ("page_table_stride", C.c_int64), ("q", C.c_void_p),
+                ("page_table_pages", C.c_int64), ("page_table_stride", C.c_int64),
+                ("q", C.c_void_p),
                 ("q_stride_layer", C.c_int64), ("q_stride_token", C.c_int64),
                 ("q_stride_head", C.c_int64), ("out", C.c_void_p),
                 ("out_stride_layer", C.c_int64), ("out_stride_token", C.c_int64),
@@ -453,7 +455,8 @@ class PagedCache:
     arguments raise at once; data-dependent errors collect in one status word,
     shared by all views, which ``check`` reads (it waits) and clears. Buffers come
     from PyTorch's caching allocator: a workspace grows to the largest call seen
-    on its stream and is kept, outside of a graph capture."""
+    on its stream and is kept; a captured call has one of the graph's own. Threads
+    may share a cache."""
 
     def __init__(self, layers: int, kv_heads: int, head_dim: int, num_pages: int,
                  page_tokens: int = 16, group: int = 128, sign_seed: int = 0,
@@ -472,7 +475,7 @@ class PagedCache:
                 pool.dtype != torch.uint8 or (pool.numel() and pool.stride(4) != 1)):
             raise ValueError(f"pool: expects a CUDA uint8 tensor {(layers, num_pages, 2, kv_heads, block)}")
         self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
-        self._ws = {}
+        self._ws, self._lock = {}, threading.Lock()
         self._set(d, pool)
 
     def _set(self, d, pool):
@@ -489,7 +492,7 @@ class PagedCache:
         if step != 1:
             raise ValueError("layers are taken in order")
         view = object.__new__(PagedCache)
-        view.status, view._ws = self.status, self._ws
+        view.status, view._ws, view._lock = self.status, self._ws, self._lock
         d = kvc_cache_desc()
         C.pointer(d)[0] = self.desc
         d.first_layer += first
@@ -504,17 +507,22 @@ class PagedCache:
         for t in tensors:
             if t is not None and t.get_device() != self.index:
                 raise ValueError(f"a tensor is on {t.device}, the cache on {self.device}")
-        return torch._C._cuda_getCurrentRawStream(self.index) if stream is None else stream.cuda_stream
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.index)
+        if stream.device_index != self.index:
+            raise ValueError(f"the stream is on device {stream.device_index}, the cache on {self.device}")
+        return stream.cuda_stream
 
     def _workspace(self, stream, handle: int, nbytes: int):
         import torch
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self._workspace(None, handle, nbytes)
         if torch.cuda.is_current_stream_capturing():  # a graph's own, from its memory pool
             return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         ws = self._ws.get(handle)
         if ws is None or ws.numel() < nbytes:
-            with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream):
-                ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-            self._ws[handle] = ws
+            ws = self._ws[handle] = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         return ws
 
     def _dtype(self, name, t):
@@ -580,11 +588,12 @@ class PagedCache:
         need = kvc_cache_load_workspace_bytes(self.desc, seq)
         if need == 0:
             raise KvcError(KVC_ERR_INVALID_ARG, "kvc_cache_load_workspace_bytes")
-        ws = self._workspace(stream, s, need)
-        _check(kvc_cache_load(stream_buf.data_ptr(), int(nbytes), self.desc, seq, slots.data_ptr(),
-                              ws.data_ptr(), ws.numel(), s), "kvc_cache_load")
-        if check:
-            _check(kvc_stream_status(ws.data_ptr(), s), "kvc_cache_load (device)")
+        with self._lock:
+            ws = self._workspace(stream, s, need)
+            _check(kvc_cache_load(stream_buf.data_ptr(), int(nbytes), self.desc, seq,
+                                  slots.data_ptr(), ws.data_ptr(), ws.numel(), s), "kvc_cache_load")
+            if check:
+                _check(kvc_stream_status(ws.data_ptr(), s), "kvc_cache_load (device)")
 
     def attend(self, q, page_table, seq_lens, q_starts=None, max_q: int = 1, out=None, lse=None,
                scale: float | None = None, causal: bool = True, window: int = 0, stream=None):
@@ -620,14 +629,16 @@ class PagedCache:
         t = kvc_cache_attn(self._dtype("q", q), shape[2] // heads, n, max_q, 1 if causal else 0,
                            window, d.head_dim ** -0.5 if scale is None else scale, 0, shape[1],
                            None if q_starts is None else q_starts.data_ptr(), seq_lens.data_ptr(),
-                           page_table.data_ptr(),
-                           page_table.stride(0) if n > 1 else page_table.shape[1],
+                           page_table.data_ptr(), page_table.shape[1],
+                           page_table.stride(0) if n > 1 else 0,
                            q.data_ptr(), *_strides(q), out.data_ptr(), *_strides(out),
                            None if lse is None else lse.data_ptr())
         call, tp = lib(), C.byref(t)
-        ws = self._workspace(stream, s, max(call.kvc_cache_attend_workspace_bytes(self._desc, tp), 1))
-        _check(call.kvc_cache_attend(self._desc, tp, ws.data_ptr(), ws.numel(), self._status, s),
-               "kvc_cache_attend")
+        with self._lock:
+            ws = self._workspace(stream, s,
+                                 max(call.kvc_cache_attend_workspace_bytes(self._desc, tp), 1))
+            _check(call.kvc_cache_attend(self._desc, tp, ws.data_ptr(), ws.numel(), self._status, s),
+                   "kvc_cache_attend")
         return out
 
     def check(self, stream=None):

@@ -143,7 +143,8 @@ kvc_status check_attn(const kvc_cache_desc *cache, const kvc_cache_attn *t, Cach
   if (!t || t->reserved != 0 || t->n_requests < 0 || t->n_requests > KVC_MAX_REQUESTS ||
       t->max_q < 1 || (t->causal != 0 && t->causal != 1) || t->window < 0 ||
       (t->window > 0 && !t->causal) || t->q_tokens < 0 || t->q_tokens > (int64_t(1) << 24) ||
-      t->page_table_stride < 0)
+      t->page_table_stride < 0 || t->page_table_pages < 0 ||
+      t->page_table_pages >= (int64_t(1) << 31) || t->page_table_stride >= (int64_t(1) << 40))
     return KVC_ERR_INVALID_ARG;
   if ((t->dtype != KVC_BF16 && t->dtype != KVC_FP16) || t->q_per_kv < 1 ||
       t->q_per_kv > KVC_CACHE_MAX_Q_PER_KV)
@@ -278,7 +279,7 @@ kvc_status kvc_cache_attend(const kvc_cache_desc *cache, const kvc_cache_attn *t
   if (!rows_ok(t->q, t->q_stride_layer, t->q_stride_token, t->q_stride_head) ||
       !rows_ok(t->out, t->out_stride_layer, t->out_stride_token, t->out_stride_head) ||
       !t->seq_lens || !aligned(t->seq_lens, 4) || !aligned(t->q_starts, 4) ||
-      !aligned(t->page_table, 4) || (t->page_table_stride > 0 && !t->page_table) ||
+      !aligned(t->page_table, 4) || (t->page_table_pages > 0 && !t->page_table) ||
       !aligned(t->lse, 4) || !workspace || !aligned(workspace, 16))
     return KVC_ERR_INVALID_ARG;
   if (workspace_bytes < w.total) return KVC_ERR_CAPACITY;
@@ -297,7 +298,7 @@ kvc_status kvc_cache_attend(const kvc_cache_desc *cache, const kvc_cache_attn *t
   a.seq_lens = t->seq_lens;
   a.page_table = t->page_table;
   a.pt_stride = t->page_table_stride;
-  const uint64_t reach = uint64_t(t->page_table_stride) * p.pt.d;
+  const uint64_t reach = uint64_t(t->page_table_pages) * p.pt.d;
   a.max_len = uint32_t(reach < 0x7FFFFFFFull ? reach : 0x7FFFFFFFull);
   a.max_blocks = uint32_t(w.blocks);
   a.row_blocks = uint32_t(w.blocks / uint64_t(t->n_requests));

@@ -551,10 +551,13 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
               if (odd_a && sc[x][i][0] != -INFINITY) sc[x][i][0] = __uint_as_float(0x7FFFFFFFu);
               if (odd_b && sc[x][i][1] != -INFINITY) sc[x][i][1] = __uint_as_float(0x7FFFFFFFu);
             }
+            // (slots that no row sees must not widen the range of scales either)
+            const bool no_a = odd_a || a0 < s.any_lo || a0 >= s.any_hi;
+            const bool no_b = odd_b || b0 < s.any_lo || b0 >= s.any_hi;
 #pragma unroll
             for (int gg = 0; gg < NG; ++gg) {
-              vA[x][gg] = odd_a ? 0u : vA[x][gg];
-              vB[x][gg] = odd_b ? 0u : vB[x][gg];
+              vA[x][gg] = no_a ? 0u : vA[x][gg];
+              vB[x][gg] = no_b ? 0u : vB[x][gg];
             }
           }
         }

@@ -116,7 +116,11 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
     uint32_t code[D / 8], meta[D / G];
     const uint32_t err = E::vector(y, code, meta, r.one, c.sym);
     if (slot == ~0u) continue;
-    if (err) note(r.status, (err & 1u) ? KVC_ERR_NONFINITE : KVC_ERR_RANGE);
+    if (err) {
+      note(r.status, (err & 1u) ? KVC_ERR_NONFINITE : KVC_ERR_RANGE);
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) code[k] = 0;  // (both forms store the same)
+    }
     const Place<D, G> pl(c, slot, at.l, at.kv, at.h);
 #pragma unroll
     for (int p = 0; p < 4; ++p) {

@@ -225,7 +225,11 @@ __global__ void __launch_bounds__(kRowThreads)
       w[j + N] = b;
     }
     if (slot == ~0u) continue;
-    if (err) note(r.status, (err & 1u) ? KVC_ERR_NONFINITE : KVC_ERR_RANGE);
+    if (err) {
+      note(r.status, (err & 1u) ? KVC_ERR_NONFINITE : KVC_ERR_RANGE);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) w[j] = 0;  // (both forms store the same)
+    }
     const Place<D, G> at(c, slot, l, kv, h);
     put_words<D>(at.codes, p, kv, w);
     // a vector with an error reads as NaN

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -435,9 +436,24 @@ class Codec:
             _check(kvc_stream_status(ws.data_ptr(), _stream_ptr(stream)), "kvc_decompress (device)")
 
 
+# kvc_cache_rows and kvc_cache_attn as bytes: PagedCache's calls on small batches take as
+# long as their host work, and filling a ctypes structure is a third of that.
+_ROWS = struct.Struct("<iiqQQ6qQ")
+_ATTN = struct.Struct("<6ifiqQQQqqQ3qQ3qQ")
+
+
+def _raw(name: str, *args):
+    """A function of the library under argument types of its own (addresses, bytes)."""
+    f = lib()[name]
+    f.restype, f.argtypes = C.c_int, args
+    return f
+
+
 def _strides(t):
-    """Strides of all dimensions but the last; those that are never stepped along, 0."""
-    return [st if n > 1 else 0 for n, st in zip(t.shape, t.stride())][:-1]
+    """Strides of the first three of four dimensions; of those never stepped along, 0."""
+    a, b, c, _ = t.shape
+    x, y, z, _ = t.stride()
+    return x if a > 1 else 0, y if b > 1 else 0, z if c > 1 else 0
 
 
 class PagedCache:
@@ -476,14 +492,21 @@ class PagedCache:
             raise ValueError(f"pool: expects a CUDA uint8 tensor {(layers, num_pages, 2, kv_heads, block)}")
         self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
         self._ws, self._lock = {}, threading.Lock()
+        A, N = C.c_void_p, C.c_size_t
+        self._calls = (_raw("kvc_cache_write", A, A, A, A), _raw("kvc_cache_read", A, A, A, A),
+                       _raw("kvc_cache_attend", A, A, A, N, A, A),
+                       {torch.bfloat16: KVC_BF16, torch.float16: KVC_FP16})
         self._set(d, pool)
 
     def _set(self, d, pool):
         d.layers = pool.shape[0]
         d.pool = pool.data_ptr() if pool.numel() else None
-        d.stride_layer, d.stride_page, d.stride_kv, d.stride_head = _strides(pool)
+        d.stride_layer, d.stride_page, d.stride_kv, d.stride_head = (
+            st if n > 1 else 0 for n, st in zip(pool.shape[:4], pool.stride()))
         self.desc, self.pool, self.device = d, pool, pool.device
-        self.index, self._desc, self._status = pool.get_device(), C.byref(d), self.status.data_ptr()
+        self.index, self._desc, self._status = pool.get_device(), C.addressof(d), self.status.data_ptr()
+        self._write, self._read, self._attend, self._types = self._calls
+        self._row = (d.layers, d.kv_heads, d.head_dim)
 
     def __getitem__(self, which) -> "PagedCache":
         if isinstance(which, int):
@@ -492,7 +515,7 @@ class PagedCache:
         if step != 1:
             raise ValueError("layers are taken in order")
         view = object.__new__(PagedCache)
-        view.status, view._ws, view._lock = self.status, self._ws, self._lock
+        view.status, view._ws, view._lock, view._calls = self.status, self._ws, self._lock, self._calls
         d = kvc_cache_desc()
         C.pointer(d)[0] = self.desc
         d.first_layer += first
@@ -513,46 +536,61 @@ class PagedCache:
             raise ValueError(f"the stream is on device {stream.device_index}, the cache on {self.device}")
         return stream.cuda_stream
 
-    def _workspace(self, stream, handle: int, nbytes: int):
+    def _workspace(self, stream, handle: int, nbytes):
+        """The stream's workspace if it has nbytes() (called where that has to be known)."""
         import torch
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self._workspace(None, handle, nbytes)
-        if torch.cuda.is_current_stream_capturing():  # a graph's own, from its memory pool
-            return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        if torch._C._cuda_isCurrentStreamCapturing():  # a graph's own, from its memory pool
+            return torch.empty(nbytes(), dtype=torch.uint8, device=self.device)
         ws = self._ws.get(handle)
-        if ws is None or ws.numel() < nbytes:
-            ws = self._ws[handle] = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        if ws is None:
+            ws = self._ws[handle] = torch.empty(nbytes(), dtype=torch.uint8, device=self.device)
+        return ws
+
+    def _with_workspace(self, where, stream, handle: int, nbytes, call):
+        """call(address, bytes) with a workspace that is large enough; one that is not is
+        refused before anything is enqueued, and replaced."""
+        with self._lock:
+            ws = self._workspace(stream, handle, nbytes)
+            st = call(ws.data_ptr(), ws.numel())
+            if st == KVC_ERR_CAPACITY:
+                self._ws.pop(handle, None)
+                ws = self._workspace(stream, handle, nbytes)
+                st = call(ws.data_ptr(), ws.numel())
+        if st:
+            raise KvcError(st, where)
         return ws
 
     def _dtype(self, name, t):
-        import torch
-        if t.dtype == torch.bfloat16:
-            return KVC_BF16
-        if t.dtype == torch.float16:
-            return KVC_FP16
-        raise KvcError(KVC_ERR_UNSUPPORTED, f"{name}: {t.dtype}")
+        kind = self._types.get(t.dtype)
+        if kind is None:
+            raise KvcError(KVC_ERR_UNSUPPORTED, f"{name}: {t.dtype}")
+        return kind
 
     def _rows(self, k, v, slots):
+        """kvc_cache_rows, as bytes."""
         import torch
-        if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
+        if slots.dtype is not torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
             raise ValueError("slots: expects a contiguous int64 vector")
-        n = slots.numel()
-        shape = (self.desc.layers, n, self.desc.kv_heads, self.desc.head_dim)
+        n, (layers, heads, dim) = slots.shape[0], self._row
+        shape = (layers, n, heads, dim)
         for name, t in (("k", k), ("v", v)):
-            if t.shape != shape or t.dtype != k.dtype or (n and t.stride(3) != 1):
+            if t.shape != shape or t.dtype is not k.dtype or (n and t.stride(3) != 1):
                 raise ValueError(f"{name}: expects {shape} of one type, head_dim contiguous; got "
                                  f"{tuple(t.shape)} {t.dtype}")
-        return kvc_cache_rows(self._dtype("k", k), 0, n, k.data_ptr(), v.data_ptr(),
-                              *_strides(k), *_strides(v), slots.data_ptr())
+        return _ROWS.pack(self._dtype("k", k), 0, n, k.data_ptr(), v.data_ptr(), *_strides(k),
+                          *_strides(v), slots.data_ptr())
 
     def write(self, k, v, slots, stream=None):
         """Quantises tokens' k and v ([layers, tokens, kv_heads, head_dim], bf16 or
-        fp16, any strides that are multiples of 8) into ``slots`` (device int64;
-        negative: skipped)."""
+        fp16, any strides that are multiples of 8) into ``slots`` (device int64, each
+        named once; negative: skipped)."""
         s = self._here(stream, k, v, slots)
-        _check(lib().kvc_cache_write(self._desc, C.byref(self._rows(k, v, slots)), self._status, s),
-               "kvc_cache_write")
+        st = self._write(self._desc, self._rows(k, v, slots), self._status, s)
+        if st:
+            raise KvcError(st, "kvc_cache_write")
 
     def read(self, slots, k=None, v=None, dtype=None, stream=None):
         """The rows stored in ``slots``, into k and v (made here if not given, with
@@ -567,8 +605,9 @@ class PagedCache:
                 k, v = (torch.zeros(d.layers, slots.numel(), d.kv_heads, d.head_dim,
                                     dtype=dtype or torch.bfloat16, device=self.device)
                         for _ in range(2))
-        _check(lib().kvc_cache_read(self._desc, C.byref(self._rows(k, v, slots)), self._status, s),
-               "kvc_cache_read")
+        st = self._read(self._desc, self._rows(k, v, slots), self._status, s)
+        if st:
+            raise KvcError(st, "kvc_cache_read")
         return k, v
 
     def load(self, stream_buf, nbytes: int, slots, seq_lens, stream=None, check: bool = False):
@@ -576,24 +615,22 @@ class PagedCache:
         order). Its own status word is read with check=True (which waits); else it
         goes unread, and a bad stream shows only in ``load``'s workspace."""
         import torch
-        if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
+        if slots.dtype is not torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
             raise ValueError("slots: expects a contiguous int64 vector")
-        if slots.numel() != sum(seq_lens):
-            raise ValueError(f"{slots.numel()} slots for {sum(seq_lens)} tokens")
+        if slots.shape[0] != sum(seq_lens):
+            raise ValueError(f"{slots.shape[0]} slots for {sum(seq_lens)} tokens")
         if stream_buf.dtype != torch.uint8 or stream_buf.numel() < int(nbytes) or \
                 not stream_buf.is_contiguous():
             raise ValueError("stream_buf: expects a contiguous uint8 buffer of nbytes")
         s = self._here(stream, stream_buf, slots)
-        seq = [int(x) for x in seq_lens]
-        need = kvc_cache_load_workspace_bytes(self.desc, seq)
-        if need == 0:
-            raise KvcError(KVC_ERR_INVALID_ARG, "kvc_cache_load_workspace_bytes")
-        with self._lock:
-            ws = self._workspace(stream, s, need)
-            _check(kvc_cache_load(stream_buf.data_ptr(), int(nbytes), self.desc, seq,
-                                  slots.data_ptr(), ws.data_ptr(), ws.numel(), s), "kvc_cache_load")
-            if check:
-                _check(kvc_stream_status(ws.data_ptr(), s), "kvc_cache_load (device)")
+        n = len(seq_lens)
+        seq, L, D = (C.c_int32 * (n or 1))(*seq_lens), lib(), C.byref(self.desc)
+        ws = self._with_workspace(
+            "kvc_cache_load", stream, s, lambda: L.kvc_cache_load_workspace_bytes(D, seq, n),
+            lambda at, size: L.kvc_cache_load(stream_buf.data_ptr(), int(nbytes), D, seq, n,
+                                              slots.data_ptr(), at, size, s))
+        if check:
+            _check(kvc_stream_status(ws.data_ptr(), s), "kvc_cache_load (device)")
 
     def attend(self, q, page_table, seq_lens, q_starts=None, max_q: int = 1, out=None, lse=None,
                scale: float | None = None, causal: bool = True, window: int = 0, stream=None):
@@ -604,41 +641,41 @@ class PagedCache:
         max_q: the most queries of one request. Returns out (made here with zeros
         if not given); lse, if given, is fp32 [layers, rows, heads]."""
         import torch
-        d = self.desc
+        (layers, heads, dim), int32 = self._row, torch.int32
         s = self._here(stream, q, page_table, seq_lens, q_starts, out, lse)
-        n, shape, heads, int32 = seq_lens.numel(), q.shape, max(d.kv_heads, 1), torch.int32
-        if len(shape) != 4 or shape[0] != d.layers or shape[3] != d.head_dim or \
-                shape[2] % heads or (shape[1] and q.stride(3) != 1):
-            raise ValueError(f"q: expects [{d.layers}, rows, a multiple of {d.kv_heads}, {d.head_dim}]")
-        if page_table.dtype != int32 or page_table.dim() != 2 or page_table.shape[0] != n or \
+        n, shape, heads = seq_lens.numel(), q.shape, heads or 1
+        if len(shape) != 4 or shape[0] != layers or shape[3] != dim or shape[2] % heads or \
+                (shape[1] and q.stride(3) != 1):
+            raise ValueError(f"q: expects [{layers}, rows, a multiple of {heads}, {dim}]")
+        if page_table.dtype is not int32 or page_table.dim() != 2 or page_table.shape[0] != n or \
                 (page_table.numel() and page_table.stride(1) != 1):
             raise ValueError(f"page_table: expects int32 [{n}, pages]")
-        if seq_lens.dtype != int32 or seq_lens.dim() != 1 or (n > 1 and seq_lens.stride(0) != 1):
+        if seq_lens.dtype is not int32 or seq_lens.dim() != 1 or (n > 1 and seq_lens.stride(0) != 1):
             raise ValueError("seq_lens: expects an int32 vector")
-        if q_starts is not None and (q_starts.dtype != int32 or q_starts.shape != (n + 1,) or
+        if q_starts is not None and (q_starts.dtype is not int32 or q_starts.shape != (n + 1,) or
                                      not q_starts.is_contiguous()):
             raise ValueError(f"q_starts: expects int32 [{n + 1}]")
         if out is None:
             with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream):
                 out = torch.zeros(shape, dtype=q.dtype, device=self.device)
-        elif out.shape != shape or out.dtype != q.dtype or (shape[1] and out.stride(3) != 1):
+        elif out.shape != shape or out.dtype is not q.dtype or (shape[1] and out.stride(3) != 1):
             raise ValueError("out: expects the shape and type of q")
-        if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:3] or
+        if lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:3] or
                                 not lse.is_contiguous()):
             raise ValueError("lse: expects contiguous float32 [layers, rows, heads]")
-        t = kvc_cache_attn(self._dtype("q", q), shape[2] // heads, n, max_q, 1 if causal else 0,
-                           window, d.head_dim ** -0.5 if scale is None else scale, 0, shape[1],
-                           None if q_starts is None else q_starts.data_ptr(), seq_lens.data_ptr(),
+        try:
+            t = _ATTN.pack(self._dtype("q", q), shape[2] // heads, n, max_q, 1 if causal else 0, window,
+                           dim ** -0.5 if scale is None else scale, 0, shape[1],
+                           0 if q_starts is None else q_starts.data_ptr(), seq_lens.data_ptr(),
                            page_table.data_ptr(), page_table.shape[1],
-                           page_table.stride(0) if n > 1 else 0,
-                           q.data_ptr(), *_strides(q), out.data_ptr(), *_strides(out),
-                           None if lse is None else lse.data_ptr())
-        call, tp = lib(), C.byref(t)
-        with self._lock:
-            ws = self._workspace(stream, s,
-                                 max(call.kvc_cache_attend_workspace_bytes(self._desc, tp), 1))
-            _check(call.kvc_cache_attend(self._desc, tp, ws.data_ptr(), ws.numel(), self._status, s),
-                   "kvc_cache_attend")
+                           page_table.stride(0) if n > 1 else 0, q.data_ptr(), *_strides(q),
+                           out.data_ptr(), *_strides(out), 0 if lse is None else lse.data_ptr())
+        except (struct.error, OverflowError) as e:
+            raise ValueError(f"max_q, window, scale: {e}") from None
+        self._with_workspace(
+            "kvc_cache_attend", stream, s, lambda: max(1, lib().kvc_cache_attend_workspace_bytes(
+                C.byref(self.desc), C.cast(t, C.POINTER(kvc_cache_attn)))),
+            lambda at, size: self._attend(self._desc, t, at, size, self._status, s))
         return out
 
     def check(self, stream=None):

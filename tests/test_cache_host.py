@@ -223,3 +223,12 @@ def test_paged_cache_refuses_in_python():
         kvc.PagedCache(1, 2, 128, 4, page_tokens=20)
     with pytest.raises(ValueError):
         kvc.PagedCache(1, 2, 128, 4, pool=torch.zeros(1, 4, 2, 2, 16 * 68, dtype=torch.uint8))
+
+
+def test_packed_structures():
+    """The bytes that PagedCache's calls pass are the structures'."""
+    a = rows(dtype=1, tokens=1 << 20, slots=FAKE + 64)
+    assert bytes(a) == kvc._ROWS.pack(1, 0, 1 << 20, FAKE, FAKE, 5120, 1024, 128, 5120, 1024, 128, FAKE + 64)
+    t = attn(dtype=1, window=5, scale=0.25, q_starts=FAKE + 4, lse=FAKE + 8)
+    assert bytes(t) == kvc._ATTN.pack(1, 4, 3, 1, 1, 5, 0.25, 0, 3, FAKE + 4, FAKE, FAKE, 10, 10, FAKE,
+                                      3 * 4096, 4096, 128, FAKE, 3 * 4096, 4096, 128, FAKE + 8)

@@ -247,7 +247,8 @@ def test_slots_outside_the_pool():
     e.write(k[:, :8], v[:, :8], s[:8])
     assert torch.equal(c.pool, e.pool)
     # without a status word
-    assert kvc.kvc_cache_write(c.desc, c._rows(k, v, s), None, torch.cuda.current_stream().cuda_stream) == kvc.KVC_OK
+    r = kvc.kvc_cache_rows(kvc.KVC_BF16, 0, n, k.data_ptr(), v.data_ptr(), *(0, 2 * d, d) * 2, s.data_ptr())
+    assert kvc.kvc_cache_write(c.desc, r, None, torch.cuda.current_stream().cuda_stream) == kvc.KVC_OK
     torch.cuda.synchronize()
     assert status_of(c) == kvc.KVC_OK
     # the same slot read many times

@@ -61,8 +61,13 @@ struct PfCfg {
   static constexpr size_t bars = wodd + kPfStages * 4 * 4;
   static constexpr size_t ctl = bars + (2 * kPfStages + 5) * 8 + 8;  // tensor memory, dead
   static constexpr size_t bytes = ctl + 16;
-  // columns of tensor memory: scores and weights 2 x 128, outputs 2 x 128
-  static constexpr uint32_t tS = 0, tO = 256;
+  // Columns of tensor memory: scores and weights of two tiles, two outputs, and where they
+  // fit beside these (not with two or four groups at d = 128) the queries, which then
+  // leave shared memory's bandwidth to the keys: 128 x 16 of them a product, twice the
+  // bytes of its keys.
+  static constexpr bool QT = D == 64 || NG == 1;
+  static constexpr uint32_t tS = 0, SW = NG * NK, tO = 2 * SW, tQ = tO + 2 * D;
+  static_assert(tQ + (QT ? D : 0) <= 512, "tensor memory");
   static_assert(bars % 8 == 0 && fc % 16 == 0 && bytes + 1024 <= 227 * 1024, "shared memory");
 };
 
@@ -446,15 +451,19 @@ __device__ __forceinline__ void pf_issue(const CacheAttnArgs &a, uint8_t *smem, 
     tm_fence_after();
     __syncwarp();
     const uint64_t dq = tm_desc(q_s, 16, 1024), dk = tm_desc(k_s + buf * C::KBUF, 16, 1024);
-    const uint32_t ts = tm + C::tS + w * 128;
+    const uint32_t ts = tm + C::tS + w * C::SW;
     if (tm_elect()) {
 #pragma unroll
       for (int g = 0; g < NG; ++g)
 #pragma unroll
         for (int st = 0; st < 2 * SG; ++st) {  // hi parts, then lo
           const int s = g * SG + st % SG, o = (s & 3) * 2;
-          tm_mma(ts + g * NK, dq + (((st / SG) * C::QPART + (s >> 2) * kPfRows * 128) >> 4) + o,
-                 dk + (((s >> 2) * NK * 128) >> 4) + o, tm_idesc(NK, false), st != 0);
+          const uint64_t k = dk + (((s >> 2) * NK * 128) >> 4) + o;
+          if constexpr (C::QT)
+            tm_mma_ts(ts + g * NK, tm + C::tQ + (st / SG) * (D / 2) + s * 8, k, tm_idesc(NK, false), st != 0);
+          else
+            tm_mma(ts + g * NK, dq + (((st / SG) * C::QPART + (s >> 2) * kPfRows * 128) >> 4) + o, k,
+                   tm_idesc(NK, false), st != 0);
         }
       tm_commit(sready + w);
     }
@@ -476,7 +485,7 @@ __device__ __forceinline__ void pf_issue(const CacheAttnArgs &a, uint8_t *smem, 
       tm_fence_after();
       __syncwarp();
       const uint64_t dv = tm_desc(v_s + buf * C::KBUF, NK * 128, 1024);
-      const uint32_t ts = tm + C::tS + w * 128, to = tm + C::tO + w * 128;
+      const uint32_t ts = tm + C::tS + w * C::SW, to = tm + C::tO + w * D;
       if (tm_elect()) {
 #pragma unroll
         for (int st = 0; st < NK / 16; ++st)
@@ -543,7 +552,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPfSoftRegs));
     const int which = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t tl = tm + (uint32_t((warp & 3) * 32) << 16);  // this warp's lanes
-    const uint32_t tO = tl + C::tO + which * 128;
+    const uint32_t tO = tl + C::tO + which * D;
     float *fcs = reinterpret_cast<float *>(smem + C::fc), *qss = reinterpret_cast<float *>(smem + C::qs);
     float2 *fin = reinterpret_cast<float2 *>(smem + C::fin);
     uint32_t j0 = 0;  // tiles before the segment
@@ -551,33 +560,32 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     while (f < f_end) {
       const PfSegment s = pf_segment_at(a, f_end, f);
       if (s.tiles == 0) continue;
-      // ---- the block's queries: qt as hi and lo parts, factors, group sums
-#pragma unroll 2
-      for (int q = 0; q < kPfRows / 8; ++q) {
-        const int rr = q * 8 + warp;  // (few rows: each warp has some)
-        const int i = lane & 7, pos = i < 4 ? 2 * i : 2 * (i - 4) + 1;
-        uint8_t *dst = smem + C::q + rr * 128 + 2 * pos;
-        if (uint32_t(rr) >= s.nc) {  // rows that are not there: zeros
-          if (lane == 0) {
-            fcs[rr] = 8.f;
+      // ---- the block's queries: qt as hi and lo parts, factors, group sums. A warp takes
+      // four rows at a time, their loads first (one at a time: 28000 cycles a segment).
+      for (int q = 0; q < kPfRows / 8; q += 4) {
+        uint16_t in[4][W];
 #pragma unroll
-            for (int g = 0; g < NG; ++g) qss[g * kPfRows + rr] = 0.f;
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t rr = (q + x) * 8 + warp;  // (few rows: each warp has some)
+          const uint32_t gr = s.c0 + (rr < s.nc ? rr : 0), qi = gr / a.qpk;
+          const uint8_t *src = a.q + int64_t(s.l) * a.q_l + int64_t(s.rs.q0 + qi) * a.q_t +
+                               int64_t(s.h * a.qpk + (gr - qi * a.qpk)) * a.q_h;
+#pragma unroll
+          for (int c = 0; c < W; ++c)
+            in[x][c] = rr < s.nc ? __ldg(reinterpret_cast<const uint16_t *>(src) + lane + 32 * c) : uint16_t(0);
+        }
+        if (uint32_t(q * 8 + warp) >= s.nc) {  // rows that are not there: zeros
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int rr = (q + x) * 8 + warp;
+            if (lane == 0) fcs[rr] = 8.f;
+            if (lane < NG) qss[lane * kPfRows + rr] = 0.f;
+#pragma unroll
+            for (int y = 0; y < 2 * C::SL; ++y)
+              *reinterpret_cast<uint32_t *>(smem + C::q + y * kPfRows * 128 + rr * 128 + 4 * lane) = 0;
           }
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int sl = 0; sl < C::SL; ++sl)
-              *reinterpret_cast<uint32_t *>(smem + C::q + x * C::QPART + sl * kPfRows * 128 +
-                                            rr * 128 + 4 * lane) = 0;
           continue;
         }
-        const uint32_t gr = s.c0 + rr, qi = gr / a.qpk;
-        const uint8_t *src = a.q + int64_t(s.l) * a.q_l + int64_t(s.rs.q0 + qi) * a.q_t +
-                             int64_t(s.h * a.qpk + (gr - qi * a.qpk)) * a.q_h;
-        uint16_t in[W];
-#pragma unroll
-        for (int c = 0; c < W; ++c)
-          in[c] = __ldg(reinterpret_cast<const uint16_t *>(src) + lane + 32 * c);
         uint64_t w0 = a.c.w0, w1 = a.c.w1;
         if (a.c.vec_signs) {
           uint64_t st = a.c.seed + (uint64_t(s.l) * 2 * a.c.heads + s.h) * uint64_t(D / 64) *
@@ -585,67 +593,105 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           w0 = splitmix64(st);
           if constexpr (D == 128) w1 = splitmix64(st);
         }
-        float y[W];
+        float y[4][W];
 #pragma unroll
-        for (int c = 0; c < W; ++c) {
-          const float x = dtype == KVC_BF16 ? __uint_as_float(uint32_t(in[c]) << 16)
-                                            : __half2float(__ushort_as_half(in[c]));
-          const uint32_t sg = uint32_t((c < 2 ? w0 : w1) >> (32 * (c & 1) + lane)) & 1u;
-          y[c] = __uint_as_float(__float_as_uint(x) ^ (sg << 31));
-        }
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int c = 0; c < W; ++c) {
+            const float u = dtype == KVC_BF16 ? __uint_as_float(uint32_t(in[x][c]) << 16)
+                                              : __half2float(__ushort_as_half(in[x][c]));
+            const uint32_t sg = uint32_t((c < 2 ? w0 : w1) >> (32 * (c & 1) + lane)) & 1u;
+            y[x][c] = __uint_as_float(__float_as_uint(u) ^ (sg << 31));
+          }
 #pragma unroll
         for (int st = 1; st < 32; st <<= 1)
 #pragma unroll
-          for (int c = 0; c < W; ++c) {
-            const float o = __shfl_xor_sync(0xFFFFFFFFu, y[c], st);
-            y[c] = (lane & st) ? o - y[c] : y[c] + o;
-          }
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int c = 0; c < W; ++c) {
+              const float o = __shfl_xor_sync(0xFFFFFFFFu, y[x][c], st);
+              y[x][c] = (lane & st) ? o - y[x][c] : y[x][c] + o;
+            }
 #pragma unroll
         for (int st = 1; st < W; st <<= 1)
 #pragma unroll
-          for (int c = 0; c < W; ++c)
-            if ((c & st) == 0) {
-              const float u = y[c], v = y[c + st];
-              y[c] = u + v;
-              y[c + st] = u - v;
-            }
-        float mx = 0.f, gs[NG];
+          for (int x = 0; x < 4; ++x)
 #pragma unroll
-        for (int g = 0; g < NG; ++g) gs[g] = 0.f;
+            for (int c = 0; c < W; ++c)
+              if ((c & st) == 0) {
+                const float u = y[x][c], v = y[x][c + st];
+                y[x][c] = u + v;
+                y[x][c + st] = u - v;
+              }
+        float mx[4], gs[4][NG];
 #pragma unroll
-        for (int c = 0; c < W; ++c) {
-          y[c] *= a.scale;
-          mx = fmaxf(mx, fabsf(y[c]));
-          gs[c * 32 / G] += y[c];
+        for (int x = 0; x < 4; ++x) {
+          mx[x] = 0.f;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) gs[x][g] = 0.f;
+#pragma unroll
+          for (int c = 0; c < W; ++c) {
+            y[x][c] *= a.scale;
+            mx[x] = fmaxf(mx[x], fabsf(y[x][c]));
+            gs[x][c * 32 / G] += y[x][c];
+          }
         }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+        for (int o = 16; o; o >>= 1)
 #pragma unroll
-          for (int g = 0; g < NG; ++g) gs[g] += __shfl_xor_sync(0xFFFFFFFFu, gs[g], o);
-        }
-        const int e = int((__float_as_uint(mx) >> 23) & 255u) - 126;
-        const bool fine = mx > 0.f && isfinite(mx) && e > -100;
-        const float es = fine ? __uint_as_float(uint32_t(127 + 14 - e) << 23) : 1.f;
-        if (lane == 0) {
-          fcs[rr] = 8.f / es;
+          for (int x = 0; x < 4; ++x) {
+            mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xFFFFFFFFu, mx[x], o));
 #pragma unroll
-          for (int g = 0; g < NG; ++g) qss[g * kPfRows + rr] = gs[g] * es;
-        }
+            for (int g = 0; g < NG; ++g) gs[x][g] += __shfl_xor_sync(0xFFFFFFFFu, gs[x][g], o);
+          }
 #pragma unroll
-        for (int c = 0; c < W; ++c) {
-          float vh, vl;
-          split_f16(y[c] * es, vh, vl);
-          const uint32_t o = (c >> 1) * kPfRows * 128 + (((4 * (c & 1) + (lane >> 3)) ^ (rr & 7)) << 4);
-          *reinterpret_cast<uint16_t *>(dst + o) = __half_as_ushort(__float2half_rn(vh));
-          *reinterpret_cast<uint16_t *>(dst + o + C::QPART) = __half_as_ushort(__float2half_rn(vl));
+        for (int x = 0; x < 4; ++x) {
+          const int rr = (q + x) * 8 + warp;
+          const int e = int((__float_as_uint(mx[x]) >> 23) & 255u) - 126;
+          const bool fine = mx[x] > 0.f && isfinite(mx[x]) && e > -100;
+          const float es = fine ? __uint_as_float(uint32_t(127 + 14 - e) << 23) : 1.f;
+          if (lane == 0) {
+            fcs[rr] = 8.f / es;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) qss[g * kPfRows + rr] = gs[x][g] * es;
+          }
+          const int i = lane & 7, pos = i < 4 ? 2 * i : 2 * (i - 4) + 1;
+          uint8_t *dst = smem + C::q + rr * 128 + 2 * pos;
+#pragma unroll
+          for (int c = 0; c < W; ++c) {
+            float vh, vl;
+            split_f16(y[x][c] * es, vh, vl);
+            const uint32_t o = (c >> 1) * kPfRows * 128 + (((4 * (c & 1) + (lane >> 3)) ^ (rr & 7)) << 4);
+            *reinterpret_cast<uint16_t *>(dst + o) = __half_as_ushort(__float2half_rn(vh));
+            *reinterpret_cast<uint16_t *>(dst + o + C::QPART) = __half_as_ushort(__float2half_rn(vl));
+          }
         }
       }
-      fence_proxy_async_smem();
-      tm_fence_before();  // (the segment before has been read)
-      __syncwarp();
-      if (lane == 0) mbar_arrive(qready);
-      named_bar_sync(1, kPfSoft);  // every row's factor and sums
+      if constexpr (!C::QT) {
+        fence_proxy_async_smem();
+        tm_fence_before();  // (the segment before has been read)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qready);
+      }
+      named_bar_sync(1, kPfSoft);  // every row's factor, sums and parts
+      if constexpr (C::QT) {  // this row's hi (first softmax) or lo parts to tensor memory
+        const uint8_t *src = smem + C::q + which * C::QPART + row * 128;
+#pragma unroll
+        for (int x = 0; x < D / 2; x += 8) {
+          uint32_t u[8];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int piece = (x / 4 + e) & 7, sl = (x / 4 + e) >> 3;
+            const uint4 v = *reinterpret_cast<const uint4 *>(src + sl * kPfRows * 128 + ((piece ^ (row & 7)) << 4));
+            u[4 * e] = v.x, u[4 * e + 1] = v.y, u[4 * e + 2] = v.z, u[4 * e + 3] = v.w;
+          }
+          tm_st8(tl + C::tQ + which * (D / 2) + x, u);
+        }
+        tm_wait_st();
+        tm_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qready);
+      }
       const float fc = fcs[row];
       float qsum[NG];
 #pragma unroll
@@ -657,7 +703,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       float nm = 0.f, mt = 0.f, thr = -INFINITY, l = 0.f, lw = 0.f, v_most = 0.f;
 
       for (uint32_t i = (which ^ j0) & 1u; i < s.tiles; i += 2) {
-        const uint32_t j = j0 + i, buf = j % kPfStages, tS = tl + C::tS + which * 128;
+        const uint32_t j = j0 + i, buf = j % kPfStages, tS = tl + C::tS + which * C::SW;
         const int32_t t0 = int32_t((s.first + i) * NK);
         pf_wait(full + buf, (j / kPfStages) & 1u, dead, a.status);  // the keys' numbers
         pf_wait(sready + which, (j >> 1) & 1u, dead, a.status);
@@ -788,7 +834,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       for (int x = 0; x < D / 2; x += 16) {  // half of the columns each
         float o[16], o1[16];
         tm_ld16(tl + C::tO + which * (D / 2) + x, o);
-        tm_ld16(tl + C::tO + 128 + which * (D / 2) + x, o1);
+        tm_ld16(tl + C::tO + D + which * (D / 2) + x, o1);
         tm_wait_ld();
         tm_loaded16(o);
         tm_loaded16(o1);

@@ -36,9 +36,9 @@ namespace kvc {
 
 constexpr int kPfRows = 128;
 constexpr int kPfSoft = 256, kPfUnpack = 256, kPfThreads = kPfSoft + kPfUnpack + 128;
-// Registers: 640 threads start with 96 each; the softmax warps take 144, the unpacking
-// ones keep 72 and the last four 48 (2 x 128 x (144 + 72) + 128 x 48 = 640 x 96).
-constexpr int kPfSoftRegs = 144, kPfUnpackRegs = 72, kPfIssueRegs = 48;
+// Registers: 640 threads start with 96 each; the softmax warps take 136, the unpacking
+// ones keep 72 and the last four 64 (2 x 128 x (136 + 72) + 128 x 64 = 640 x 96).
+constexpr int kPfSoftRegs = 136, kPfUnpackRegs = 72, kPfIssueRegs = 64;
 constexpr uint32_t kPfStages = 4;
 constexpr uint32_t kPfLead = 3;  // a segment's fixed work, in tiles
 
@@ -57,17 +57,18 @@ struct PfCfg {
   static constexpr size_t fin = qs + size_t(NG) * kPfRows * 4;  // [softmax][row] maximum, sum
   static constexpr size_t wmax = fin + 2 * kPfRows * 8;         // [stage][unpacking warp]
   static constexpr size_t wodd = wmax + kPfStages * 4 * 4;
-  // full and values (a stage), scores and weights (a softmax), queries
+  // full and values (a stage), scores and weights (a tile's scores), queries
   static constexpr size_t bars = wodd + kPfStages * 4 * 4;
-  static constexpr size_t ctl = bars + (2 * kPfStages + 5) * 8 + 8;  // tensor memory, dead
+  static constexpr size_t ctl = bars + (2 * kPfStages + 7) * 8 + 8;  // tensor memory, dead
   static constexpr size_t bytes = ctl + 16;
-  // Columns of tensor memory: scores and weights of two tiles, two outputs, and where they
-  // fit beside these (not with two or four groups at d = 128) the queries, which then
-  // leave shared memory's bandwidth to the keys: 128 x 16 of them a product, twice the
-  // bytes of its keys.
-  static constexpr bool QT = D == 64 || NG == 1;
-  static constexpr uint32_t tS = 0, SW = NG * NK, tO = 2 * SW, tQ = tO + 2 * D;
-  static_assert(tQ + (QT ? D : 0) <= 512, "tensor memory");
+  // Columns of tensor memory: scores (and weights) of NS tiles, two outputs, and in what is
+  // left the queries' hi parts, then the lo parts. With three tiles' scores a tile's are
+  // computed during the softmax before it; queries there leave shared memory's bandwidth
+  // to the keys (128 x 16 of them a product, twice the bytes of its keys).
+  static constexpr uint32_t SW = NG * NK, NS = 3 * SW + 2 * D <= 512 ? 3 : 2;
+  static constexpr uint32_t tS = 0, tO = NS * SW, tQ = tO + 2 * D;
+  static constexpr bool QH = tQ + D / 2 <= 512, QL = tQ + D <= 512;
+  static_assert(tQ <= 512, "tensor memory");
   static_assert(bars % 8 == 0 && fc % 16 == 0 && bytes + 1024 <= 227 * 1024, "shared memory");
 };
 
@@ -433,39 +434,41 @@ __device__ __forceinline__ void pf_unpack(const CacheAttnArgs &a, uint8_t *smem,
   }
 }
 
-// The issuing warp: every tile's products, in the order QK 0, QK 1, then PV i, QK i + 2.
-// The tensor cores take them one after the other: a tile's scores are ready after the
-// values of the tile two before, whose weights they replace.
+// The issuing warp: every tile's products, QK 0 .. QK NS - 1, then PV i, QK i + NS, whose
+// scores replace tile i's weights (the tensor cores take products one after the other).
+// Its time is a tile's: places and phases are counted on, not divided out (a poll with
+// these divisions took 500 cycles).
 template <int D, int G>
 __device__ __forceinline__ void pf_issue(const CacheAttnArgs &a, uint8_t *smem, uint32_t tm,
                                          uint64_t f, uint64_t f_end) {
   using C = PfCfg<D, G>;
   constexpr int NG = C::NG, NK = C::NK, SG = G / 16;  // (16-channel steps of a group)
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::bars), *pv = full + kPfStages;
-  uint64_t *sready = pv + kPfStages, *pready = sready + 2, *qready = pready + 2;
+  constexpr uint32_t NS = C::NS, ST = kPfStages;
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::bars), *pv = full + ST;
+  uint64_t *sready = pv + ST, *pready = sready + NS, *qready = pready + NS;
   volatile uint32_t *dead = reinterpret_cast<uint32_t *>(smem + C::ctl) + 1;
   const uint32_t q_s = smem_u32(smem + C::q), k_s = smem_u32(smem + C::k), v_s = smem_u32(smem + C::v);
-  auto scores = [&](uint32_t j) {
-    const uint32_t buf = tm_uniform(j % kPfStages), w = tm_uniform(j & 1);
-    pf_wait(full + buf, (j / kPfStages) & 1u, dead, a.status);
+  // scores of the tile in stage st to place sb
+  auto scores = [&](uint32_t st, uint32_t phase, uint32_t sb) {
+    pf_wait(full + st, phase, dead, a.status);
     tm_fence_after();
     __syncwarp();
-    const uint64_t dq = tm_desc(q_s, 16, 1024), dk = tm_desc(k_s + buf * C::KBUF, 16, 1024);
-    const uint32_t ts = tm + C::tS + w * C::SW;
+    const uint64_t dq = tm_desc(q_s, 16, 1024), dk = tm_desc(k_s + st * C::KBUF, 16, 1024);
+    const uint32_t ts = tm + C::tS + sb * C::SW;
     if (tm_elect()) {
 #pragma unroll
       for (int g = 0; g < NG; ++g)
 #pragma unroll
-        for (int st = 0; st < 2 * SG; ++st) {  // hi parts, then lo
-          const int s = g * SG + st % SG, o = (s & 3) * 2;
-          const uint64_t k = dk + (((s >> 2) * NK * 128) >> 4) + o;
-          if constexpr (C::QT)
-            tm_mma_ts(ts + g * NK, tm + C::tQ + (st / SG) * (D / 2) + s * 8, k, tm_idesc(NK, false), st != 0);
+        for (int x = 0; x < 2 * SG; ++x) {  // hi parts, then lo
+          const int c = g * SG + x % SG, o = (c & 3) * 2;
+          const uint64_t k = dk + (((c >> 2) * NK * 128) >> 4) + o;
+          if (x < SG ? C::QH : C::QL)
+            tm_mma_ts(ts + g * NK, tm + C::tQ + (x / SG) * (D / 2) + c * 8, k, tm_idesc(NK, false), x != 0);
           else
-            tm_mma(ts + g * NK, dq + (((st / SG) * C::QPART + (s >> 2) * kPfRows * 128) >> 4) + o, k,
-                   tm_idesc(NK, false), st != 0);
+            tm_mma(ts + g * NK, dq + (((x / SG) * C::QPART + (c >> 2) * kPfRows * 128) >> 4) + o, k,
+                   tm_idesc(NK, false), x != 0);
         }
-      tm_commit(sready + w);
+      tm_commit(sready + sb);
     }
     __syncwarp();
   };
@@ -474,29 +477,45 @@ __device__ __forceinline__ void pf_issue(const CacheAttnArgs &a, uint8_t *smem, 
     const PfSegment s = pf_segment_at(a, f_end, f);
     if (s.tiles == 0) continue;
     const uint32_t tiles = tm_uniform(s.tiles);
+    // tile i's place and its phase; the stage and its phase of tile i, of the next scores
+    uint32_t sb = tm_uniform(j0 % NS), sp = tm_uniform((j0 / NS) & 1u), odd = tm_uniform(j0 & 1u);
+    uint32_t st = tm_uniform(j0 % ST), kt = st, kp = tm_uniform((j0 / ST) & 1u);
     pf_wait(qready, seg & 1u, dead, a.status);
     tm_fence_after();
     __syncwarp();
-    scores(j0);
-    if (tiles > 1) scores(j0 + 1);
+    auto next_keys = [&]() {
+      kp ^= kt == ST - 1 ? 1u : 0u;
+      kt = kt == ST - 1 ? 0 : kt + 1;
+    };
+    uint32_t place = sb;
+    for (uint32_t q = 0; q < NS && q < tiles; ++q) {
+      scores(kt, kp, place);
+      next_keys();
+      place = place == NS - 1 ? 0 : place + 1;
+    }
     for (uint32_t i = 0; i < tiles; ++i) {
-      const uint32_t j = j0 + i, w = tm_uniform(j & 1), buf = tm_uniform(j % kPfStages);
-      pf_wait(pready + w, (j >> 1) & 1u, dead, a.status);
+      pf_wait(pready + sb, sp, dead, a.status);
       tm_fence_after();
       __syncwarp();
-      const uint64_t dv = tm_desc(v_s + buf * C::KBUF, NK * 128, 1024);
-      const uint32_t ts = tm + C::tS + w * C::SW, to = tm + C::tO + w * D;
+      const uint64_t dv = tm_desc(v_s + st * C::KBUF, NK * 128, 1024);
+      const uint32_t ts = tm + C::tS + sb * C::SW, to = tm + C::tO + odd * D;
       if (tm_elect()) {
 #pragma unroll
-        for (int st = 0; st < NK / 16; ++st)
-          tm_mma_ts(to, ts + st * 8, dv + st * 128, tm_idesc(D, true), i > 1 || st != 0);
-        tm_commit(pv + buf);
+        for (int x = 0; x < NK / 16; ++x)
+          tm_mma_ts(to, ts + x * 8, dv + x * 128, tm_idesc(D, true), i > 1 || x != 0);
+        tm_commit(pv + st);
       }
       __syncwarp();
-      if (i + 2 < tiles) scores(j + 2);
+      if (i + NS < tiles) {
+        scores(kt, kp, sb);
+        next_keys();
+      }
+      sp ^= sb == NS - 1 ? 1u : 0u;
+      sb = sb == NS - 1 ? 0 : sb + 1;
+      st = st == ST - 1 ? 0 : st + 1;
+      odd ^= 1u;
     }
-    __syncwarp();
-    j0 += s.tiles;
+    j0 += tiles;
     ++seg;
   }
 }
@@ -509,7 +528,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::bars), *pv = full + kPfStages;
-  uint64_t *sready = pv + kPfStages, *pready = sready + 2, *qready = pready + 2;
+  uint64_t *sready = pv + kPfStages, *pready = sready + C::NS, *qready = pready + C::NS;
   uint32_t *ctl = reinterpret_cast<uint32_t *>(smem + C::ctl);
   volatile uint32_t *dead = ctl + 1;
   if (warp == 0) {
@@ -524,7 +543,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       mbar_init(full + i, 4);
       mbar_init(pv + i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (uint32_t i = 0; i < C::NS; ++i) {
       mbar_init(sready + i, 1);
       mbar_init(pready + i, 4);
     }
@@ -667,14 +686,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           }
         }
       }
-      if constexpr (!C::QT) {
-        fence_proxy_async_smem();
-        tm_fence_before();  // (the segment before has been read)
-        __syncwarp();
-        if (lane == 0) mbar_arrive(qready);
-      }
       named_bar_sync(1, kPfSoft);  // every row's factor, sums and parts
-      if constexpr (C::QT) {  // this row's hi (first softmax) or lo parts to tensor memory
+      // this row's hi (first softmax) or lo parts to tensor memory
+      if (which == 0 ? C::QH : C::QL) {
         const uint8_t *src = smem + C::q + which * C::QPART + row * 128;
 #pragma unroll
         for (int x = 0; x < D / 2; x += 8) {
@@ -688,10 +702,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           tm_st8(tl + C::tQ + which * (D / 2) + x, u);
         }
         tm_wait_st();
-        tm_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(qready);
       }
+      fence_proxy_async_smem();
+      tm_fence_before();  // (the segment before has been read)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qready);
       const float fc = fcs[row];
       float qsum[NG];
 #pragma unroll
@@ -703,10 +718,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       float nm = 0.f, mt = 0.f, thr = -INFINITY, l = 0.f, lw = 0.f, v_most = 0.f;
 
       for (uint32_t i = (which ^ j0) & 1u; i < s.tiles; i += 2) {
-        const uint32_t j = j0 + i, buf = j % kPfStages, tS = tl + C::tS + which * C::SW;
+        const uint32_t j = j0 + i, buf = j % kPfStages, sb = j % C::NS, tS = tl + C::tS + sb * C::SW;
         const int32_t t0 = int32_t((s.first + i) * NK);
         pf_wait(full + buf, (j / kPfStages) & 1u, dead, a.status);  // the keys' numbers
-        pf_wait(sready + which, (j >> 1) & 1u, dead, a.status);
+        pf_wait(sready + sb, (j / C::NS) & 1u, dead, a.status);
         tm_fence_after();
         __syncwarp();
         const float *meta = reinterpret_cast<const float *>(smem + C::meta) + buf * C::MW * NK;
@@ -770,7 +785,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           }
           nm = lw - mt;
           l *= fac;
-          if (i > 1) {  // (the values of this softmax's last tile are in: its scores came after)
+          if (i > 1) {  // this softmax's last values are in
+            pf_wait(pv + (j - 2) % kPfStages, ((j - 2) / kPfStages) & 1u, dead, a.status);
+            tm_fence_after();
+            __syncwarp();
 #pragma unroll
             for (int x = 0; x < D; x += 16) {
               float o[16];
@@ -808,7 +826,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         tm_wait_st();
         tm_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(pready + which);
+        if (lane == 0) mbar_arrive(pready + sb);
       }
 
       // ---- the segment's record, of both softmaxes' results

@@ -65,7 +65,7 @@ struct CacheAttnArgs {
   float *lse;
   uint32_t *status;
   // workspace: per request prefixes of work and shapes (queries, first row, keys),
-  // query fragments per unit, records per unit and warp
+  // queries per unit (fragments, or blocks of 128 rows), records per unit and warp
   uint64_t *wpre;  // per request, or per block of 128 rows
   uint4 *shapes;
   uint4 *blk;      // blocks of 128 rows: request, first row, first key tile, tiles
@@ -90,6 +90,9 @@ inline uint64_t cache_frag_bytes(int d, int cols) {
   if (cols > 16) return 0;
   return uint64_t(cols == 4 ? 1 : cols / 8) * uint64_t(d / 16) * 32 * (cols == 4 ? 8 : 16) + 512;
 }
+// A block of 128 rows' queries in the workspace, bytes: both parts as shared memory holds
+// them, factors and sums.
+inline uint64_t cache_block_q_bytes(int d, int g) { return 128 * (4 * uint64_t(d) + 4 * uint64_t(1 + d / g)); }
 // Warps of an attention launch at most (the workspace holds a record for each
 // beside one per unit): 16 for each of 160 SMs.
 constexpr uint32_t kCacheWarpsMax = 2560;

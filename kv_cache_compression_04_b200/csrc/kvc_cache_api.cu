@@ -129,12 +129,12 @@ kvc_status load_shape(const kvc_cache_desc *c, const int32_t *seq_lens, int32_t 
   return KVC_OK;
 }
 
-// The attention's workspace: prefixes of work and the requests' shapes; query fragments
-// per unit (layer, kv head, block of up to 16 rows of a request), or the numbers of the
-// blocks of 128 rows; then one record per unit and per warp or CTA (each cols x (4 +
+// The attention's workspace: prefixes of work and the requests' shapes; with blocks of 128
+// rows, their numbers; the transformed queries per unit (layer, kv head, block of rows of
+// a request); then one record per unit and per warp or CTA (each cols x (4 +
 // head_dim) fp32).
 struct AttnWs {
-  uint64_t blocks = 0, shapes = 0, frags = 0, rec = 0, total = 0;
+  uint64_t blocks = 0, shapes = 0, frags = 0, queries = 0, rec = 0, total = 0;
 };
 kvc_status check_attn(const kvc_cache_desc *cache, const kvc_cache_attn *t, CachePool &p, AttnWs &w,
                       bool pool_too) {
@@ -155,13 +155,14 @@ kvc_status check_attn(const kvc_cache_desc *cache, const kvc_cache_attn *t, Cach
   const uint64_t reqs = uint64_t(t->n_requests), lh = uint64_t(cache->layers) * heads;
   w.blocks = cols > 16 ? uint64_t(t->q_tokens) * qpk / cols + reqs : reqs * ((rows + cols - 1) / cols);
   const uint64_t units = lh * w.blocks;
-  // (query rows of a request, and units, are counted in 32 bits)
-  if (units >= (uint64_t(1) << 31) - 1 || uint64_t(t->q_tokens) * qpk >= (uint64_t(1) << 31))
+  // (query rows of a request, and units, are counted in 32 bits; a CTA has 32 of 128 rows)
+  if (units * (cols > 16 ? 4 : 1) >= (uint64_t(1) << 31) - 1 || uint64_t(t->q_tokens) * qpk >= (uint64_t(1) << 31))
     return KVC_ERR_UNSUPPORTED;
   w.shapes = round256(8 * ((cols > 16 ? w.blocks : reqs) + 1));
   w.frags = w.shapes + round256(16 * reqs);
-  const uint64_t frags = cols > 16 ? 16 * w.blocks : units * cache_frag_bytes(cache->head_dim, int(cols));
-  w.rec = round256(w.frags + frags);
+  w.queries = w.frags + (cols > 16 ? round256(16 * w.blocks) : 0);
+  w.rec = round256(w.queries + units * (cols > 16 ? cache_block_q_bytes(cache->head_dim, cache->group_size)
+                                                  : cache_frag_bytes(cache->head_dim, int(cols))));
   w.total = w.rec + (units + (cols > 16 ? kCachePrefillCtas : kCacheWarpsMax)) * cols *
                         (4 + uint64_t(cache->head_dim)) * sizeof(float);
   return KVC_OK;
@@ -317,7 +318,7 @@ kvc_status kvc_cache_attend(const kvc_cache_desc *cache, const kvc_cache_attn *t
   a.wpre = reinterpret_cast<uint64_t *>(ws);
   a.shapes = reinterpret_cast<uint4 *>(ws + w.shapes);
   a.blk = reinterpret_cast<uint4 *>(ws + w.frags);
-  a.qws = ws + w.frags;
+  a.qws = ws + w.queries;
   a.rec = reinterpret_cast<float *>(ws + w.rec);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const int g = cache->group_size;

@@ -46,20 +46,19 @@ template <int D, int G>
 struct PfCfg {
   static constexpr int NG = D / G, NK = NG == 4 ? 32 : 64, SL = D / 64, W = D / 32;
   static constexpr uint32_t TB = cache_tile_bytes(D, G), CB = cache_code_bytes(D);
-  static constexpr uint32_t QPART = SL * kPfRows * 128, KBUF = SL * NK * 128;
+  // queries of a block, in the workspace too: parts (then each row's factor, its sums)
+  static constexpr uint32_t QPART = SL * kPfRows * 128, QB = 2 * QPART + kPfRows * 4 * (1 + NG), KBUF = SL * NK * 128;
   static constexpr int MW = 2 * NG + 2;  // words of a key's numbers: s, z + 8 s; 2^e, bias
   static constexpr size_t q = 0;
   static constexpr size_t k = q + 2 * QPART;
   static constexpr size_t v = k + kPfStages * KBUF;
   static constexpr size_t meta = v + kPfStages * KBUF;
-  static constexpr size_t fc = meta + kPfStages * size_t(MW) * NK * 4;
-  static constexpr size_t qs = fc + kPfRows * 4;
-  static constexpr size_t fin = qs + size_t(NG) * kPfRows * 4;  // [softmax][row] maximum, sum
+  static constexpr size_t fin = meta + kPfStages * size_t(MW) * NK * 4;  // [softmax][row] maximum, sum
   static constexpr size_t wmax = fin + 2 * kPfRows * 8;         // [stage][unpacking warp]
   static constexpr size_t wodd = wmax + kPfStages * 4 * 4;
-  // full and values (a stage), scores and weights (a tile's scores), queries
+  // full and values (a stage), scores and weights (a tile's scores), queries copied, ready
   static constexpr size_t bars = wodd + kPfStages * 4 * 4;
-  static constexpr size_t ctl = bars + (2 * kPfStages + 7) * 8 + 8;  // tensor memory, dead
+  static constexpr size_t ctl = bars + (2 * kPfStages + 8) * 8;  // tensor memory, dead
   static constexpr size_t bytes = ctl + 16;
   // Columns of tensor memory: scores (and weights) of NS tiles, two outputs, and in what is
   // left the queries' hi parts, then the lo parts. With three tiles' scores a tile's are
@@ -69,7 +68,7 @@ struct PfCfg {
   static constexpr uint32_t tS = 0, tO = NS * SW, tQ = tO + 2 * D;
   static constexpr bool QH = tQ + D / 2 <= 512, QL = tQ + D <= 512;
   static_assert(tQ <= 512, "tensor memory");
-  static_assert(bars % 8 == 0 && fc % 16 == 0 && bytes + 1024 <= 227 * 1024, "shared memory");
+  static_assert(bars % 8 == 0 && fin % 16 == 0 && ctl % 8 == 0 && bytes + 1024 <= 227 * 1024, "shared memory");
 };
 
 // ------------------------------------------------------------- tcgen05 --
@@ -161,14 +160,15 @@ __device__ __forceinline__ void tm_commit(uint64_t *bar) {
 }
 
 // Bounded wait for the phase with the given parity; a wait that runs out marks the
-// CTA (*dead), whose other waits then end at once.
+// CTA (*dead), whose other waits then end at once (but not kOwn ones, for a copy in flight).
+template <bool kOwn = false>
 __device__ __forceinline__ void pf_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *dead,
                                         uint32_t *status) {
   if (mbar_try_wait(bar, parity)) return;
   const uint64_t t0 = globaltimer();
   for (uint32_t i = 1; i < kWaitIters; ++i) {
     if (mbar_try_wait(bar, parity)) return;
-    if ((i & 15u) == 0 && (*dead || globaltimer() - t0 > kWaitNs)) break;
+    if ((i & 15u) == 0 && ((!kOwn && *dead) || globaltimer() - t0 > kWaitNs)) break;
   }
   *dead = 1;
   if (status) set_status(status, KVC_ERR_TIMEOUT);
@@ -181,60 +181,165 @@ __device__ __forceinline__ uint32_t first_block(const CacheAttnArgs &a, uint32_t
   return uint32_t(uint64_t(q0) * a.qpk / kPfRows) + r;
 }
 
-// First kernel, one CTA: the requests' shapes; each block's request, first row, first
-// key tile and tiles; prefixes of the blocks' work (per layer and head).
+// A block's request, first row, first key tile and tiles (0: none of its rows sees a key).
 template <int NK>
-__global__ void __launch_bounds__(1024) cache_prefill_prep_kernel(const __grid_constant__ CacheAttnArgs a) {
-  __shared__ uint64_t red[32];
+__device__ __forceinline__ uint4 block_info(const CacheAttnArgs &a, uint32_t b, ReqShape &s) {
+  uint32_t lo = 0, hi = a.n_req - 1;  // the last request whose first block is not past b
+  while (lo < hi) {
+    const uint32_t mid = (lo + hi + 1) >> 1;
+    const uint32_t q0 = a.q_starts ? uint32_t(max(0, __ldg(a.q_starts + mid))) : mid;
+    if (first_block(a, q0, mid) <= b) lo = mid;
+    else hi = mid - 1;
+  }
+  bool ok;
+  s = read_request(a, lo, ok);
+  const uint32_t fb = first_block(a, s.q0, lo), rows = s.nq * a.qpk;
+  uint4 info = make_uint4(lo, 0, 0, 0);
+  if (ok && b >= fb && uint64_t(b - fb) * kPfRows < rows) {
+    info.y = (b - fb) * kPfRows;
+    int32_t k0, k1, x;
+    key_range(a, s, info.y / a.qpk, k0, x);
+    key_range(a, s, (min(info.y + kPfRows, rows) - 1) / a.qpk, x, k1);
+    info.z = uint32_t(k0) / NK;
+    info.w = k1 > k0 ? (uint32_t(k1) + NK - 1) / NK - info.z : 0;
+  }
+  return info;
+}
+
+// First kernel. CTA 0: the requests' shapes, the blocks' numbers and the prefixes of their
+// work (per layer and head). The others take 32 rows of a unit's queries each: transformed,
+// in fp16 hi and lo parts as the second kernel's shared memory holds them (done there, they
+// took 17000 cycles a segment, in which the tensor cores waited).
+constexpr int kPfPrep = 256, kPfPrepRows = 32;
+template <int D, int G>
+__global__ void __launch_bounds__(kPfPrep)
+    cache_prefill_prep_kernel(const __grid_constant__ CacheAttnArgs a, const int dtype) {
+  using C = PfCfg<D, G>;
+  constexpr int NG = C::NG, NK = C::NK, W = C::W;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.n_req;
-  for (uint32_t r = tid; r < n; r += 1024) {
-    bool ok;
-    const ReqShape s = read_request(a, r, ok);
-    if (!ok && a.status) set_status(a.status, KVC_ERR_CORRUPT);
-    a.shapes[r] = make_uint4(s.nq, s.q0, s.len, 0);
-  }
-  const uint32_t nb = a.max_blocks, per = (nb + 1023) / 1024;
-  const uint32_t b0 = min(nb, tid * per), b1 = min(nb, b0 + per);
-  uint64_t w = 0;
-  for (uint32_t b = b0; b < b1; ++b) {
-    uint32_t lo = 0, hi = n - 1;  // the last request whose first block is not past b
-    while (lo < hi) {
-      const uint32_t mid = (lo + hi + 1) >> 1;
-      const uint32_t q0 = a.q_starts ? uint32_t(max(0, __ldg(a.q_starts + mid))) : mid;
-      if (first_block(a, q0, mid) <= b) lo = mid;
-      else hi = mid - 1;
+  const uint32_t nb = a.max_blocks;
+  if (blockIdx.x == 0) {
+    __shared__ uint64_t red[kPfPrep / 32];
+    for (uint32_t r = tid; r < n; r += kPfPrep) {
+      bool ok;
+      const ReqShape s = read_request(a, r, ok);
+      if (!ok && a.status) set_status(a.status, KVC_ERR_CORRUPT);
+      a.shapes[r] = make_uint4(s.nq, s.q0, s.len, 0);
     }
-    bool ok;
-    const ReqShape s = read_request(a, lo, ok);
-    const uint32_t fb = first_block(a, s.q0, lo), rows = s.nq * a.qpk;
-    uint4 info = make_uint4(lo, 0, 0, 0);
-    if (ok && b >= fb && uint64_t(b - fb) * kPfRows < rows) {
-      info.y = (b - fb) * kPfRows;
-      int32_t k0, k1, x;
-      key_range(a, s, info.y / a.qpk, k0, x);
-      key_range(a, s, (min(info.y + kPfRows, rows) - 1) / a.qpk, x, k1);
-      info.z = uint32_t(k0) / NK;
-      info.w = k1 > k0 ? (uint32_t(k1) + NK - 1) / NK - info.z : 0;
+    const uint32_t per = (nb + kPfPrep - 1) / kPfPrep;
+    const uint32_t b0 = min(nb, tid * per), b1 = min(nb, b0 + per);
+    uint64_t w = 0;
+    for (uint32_t b = b0; b < b1; ++b) {
+      ReqShape s;
+      const uint4 info = block_info<NK>(a, b, s);
+      a.blk[b] = info;
+      w += info.w ? info.w + kPfLead : 0;
     }
-    a.blk[b] = info;
-    w += info.w ? info.w + kPfLead : 0;
-  }
-  uint64_t wi = w;
+    uint64_t wi = w;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t x = __shfl_up_sync(0xFFFFFFFFu, wi, o);
-    if (int(lane) >= o) wi += x;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t x = __shfl_up_sync(0xFFFFFFFFu, wi, o);
+      if (int(lane) >= o) wi += x;
+    }
+    if (lane == 31) red[warp] = wi;
+    __syncthreads();
+    uint64_t base = wi - w;
+    for (uint32_t k = 0; k < warp; ++k) base += red[k];
+    for (uint32_t b = b0; b < b1; ++b) {
+      a.wpre[b] = base;
+      const uint32_t t = a.blk[b].w;
+      base += t ? t + kPfLead : 0;
+    }
+    if (tid == kPfPrep - 1) a.wpre[nb] = base;
+    return;
   }
-  if (lane == 31) red[warp] = wi;
-  __syncthreads();
-  uint64_t base = wi - w;
-  for (uint32_t k = 0; k < warp; ++k) base += red[k];
-  for (uint32_t b = b0; b < b1; ++b) {
-    a.wpre[b] = base;
-    const uint32_t t = a.blk[b].w;
-    base += t ? t + kPfLead : 0;
+  constexpr uint32_t kParts = kPfRows / kPfPrepRows;
+  const uint32_t unit = (blockIdx.x - 1) / kParts, r0 = (blockIdx.x - 1 - unit * kParts) * kPfPrepRows;
+  const uint32_t lh = unit / nb, l = lh / a.c.heads, h = lh - l * a.c.heads;
+  ReqShape rs;
+  const uint4 info = block_info<NK>(a, unit - lh * nb, rs);
+  if (info.w == 0) return;
+  const uint32_t nc = min(uint32_t(kPfRows), rs.nq * a.qpk - info.y);
+  uint64_t w0 = a.c.w0, w1 = a.c.w1;
+  if (a.c.vec_signs) {
+    uint64_t st = a.c.seed + (uint64_t(l) * 2 * a.c.heads + h) * uint64_t(D / 64) * 0x9E3779B97F4A7C15ull;
+    w0 = splitmix64(st);
+    if constexpr (D == 128) w1 = splitmix64(st);
   }
-  if (tid == 1023) a.wpre[nb] = base;
+  uint8_t *image = a.qws + uint64_t(unit) * C::QB;
+  float *qx = reinterpret_cast<float *>(image + 2 * C::QPART);
+#pragma unroll
+  for (uint32_t x = 0; x < kPfPrepRows; x += kPfPrep / 32) {
+    const uint32_t rr = r0 + x + warp;
+    const int i = lane & 7, pos = i < 4 ? 2 * i : 2 * (i - 4) + 1;
+    uint8_t *dst = image + rr * 128 + 2 * pos;
+    if (rr >= nc) {  // rows that are not there: zeros
+      if (lane <= NG) qx[lane * kPfRows + rr] = lane ? 0.f : 8.f;
+#pragma unroll
+      for (int y = 0; y < 2 * C::SL; ++y)
+        *reinterpret_cast<uint32_t *>(image + y * kPfRows * 128 + rr * 128 + 4 * lane) = 0;
+      continue;
+    }
+    const uint32_t gr = info.y + rr, qi = gr / a.qpk;
+    const uint8_t *src = a.q + int64_t(l) * a.q_l + int64_t(rs.q0 + qi) * a.q_t +
+                         int64_t(h * a.qpk + (gr - qi * a.qpk)) * a.q_h;
+    float y[W];
+#pragma unroll
+    for (int c = 0; c < W; ++c) {
+      const uint16_t in = __ldg(reinterpret_cast<const uint16_t *>(src) + lane + 32 * c);
+      const float x = dtype == KVC_BF16 ? __uint_as_float(uint32_t(in) << 16)
+                                        : __half2float(__ushort_as_half(in));
+      const uint32_t sg = uint32_t((c < 2 ? w0 : w1) >> (32 * (c & 1) + lane)) & 1u;
+      y[c] = __uint_as_float(__float_as_uint(x) ^ (sg << 31));
+    }
+#pragma unroll
+    for (int st = 1; st < 32; st <<= 1)
+#pragma unroll
+      for (int c = 0; c < W; ++c) {
+        const float o = __shfl_xor_sync(0xFFFFFFFFu, y[c], st);
+        y[c] = (lane & st) ? o - y[c] : y[c] + o;
+      }
+#pragma unroll
+    for (int st = 1; st < W; st <<= 1)
+#pragma unroll
+      for (int c = 0; c < W; ++c)
+        if ((c & st) == 0) {
+          const float u = y[c], v = y[c + st];
+          y[c] = u + v;
+          y[c + st] = u - v;
+        }
+    float mx = 0.f, gs[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) gs[g] = 0.f;
+#pragma unroll
+    for (int c = 0; c < W; ++c) {
+      y[c] *= a.scale;
+      mx = fmaxf(mx, fabsf(y[c]));
+      gs[c * 32 / G] += y[c];
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+#pragma unroll
+      for (int g = 0; g < NG; ++g) gs[g] += __shfl_xor_sync(0xFFFFFFFFu, gs[g], o);
+    }
+    const int e = int((__float_as_uint(mx) >> 23) & 255u) - 126;
+    const bool fine = mx > 0.f && isfinite(mx) && e > -100;
+    const float es = fine ? __uint_as_float(uint32_t(127 + 14 - e) << 23) : 1.f;
+    if (lane == 0) {
+      qx[rr] = 8.f / es;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) qx[(1 + g) * kPfRows + rr] = gs[g] * es;
+    }
+#pragma unroll
+    for (int c = 0; c < W; ++c) {
+      float vh, vl;
+      split_f16(y[c] * es, vh, vl);
+      const uint32_t o = (c >> 1) * kPfRows * 128 + (((4 * (c & 1) + (lane >> 3)) ^ (rr & 7)) << 4);
+      *reinterpret_cast<uint16_t *>(dst + o) = __half_as_ushort(__float2half_rn(vh));
+      *reinterpret_cast<uint16_t *>(dst + o + C::QPART) = __half_as_ushort(__float2half_rn(vl));
+    }
+  }
 }
 
 // A CTA's part of a unit.
@@ -529,6 +634,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::bars), *pv = full + kPfStages;
   uint64_t *sready = pv + kPfStages, *pready = sready + C::NS, *qready = pready + C::NS;
+  uint64_t *qcopied = qready + 1;
   uint32_t *ctl = reinterpret_cast<uint32_t *>(smem + C::ctl);
   volatile uint32_t *dead = ctl + 1;
   if (warp == 0) {
@@ -548,6 +654,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       mbar_init(pready + i, 4);
     }
     mbar_init(qready, kPfSoft / 32);
+    mbar_init(qcopied, 1);
     mbar_fence_init();
     *dead = 0;
   }
@@ -572,121 +679,29 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const int which = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t tl = tm + (uint32_t((warp & 3) * 32) << 16);  // this warp's lanes
     const uint32_t tO = tl + C::tO + which * D;
-    float *fcs = reinterpret_cast<float *>(smem + C::fc), *qss = reinterpret_cast<float *>(smem + C::qs);
     float2 *fin = reinterpret_cast<float2 *>(smem + C::fin);
-    uint32_t j0 = 0;  // tiles before the segment
+    uint32_t j0 = 0, seg = 0;  // tiles and segments before
 
     while (f < f_end) {
       const PfSegment s = pf_segment_at(a, f_end, f);
       if (s.tiles == 0) continue;
-      // ---- the block's queries: qt as hi and lo parts, factors, group sums. A warp takes
-      // four rows at a time, their loads first (one at a time: 28000 cycles a segment).
-      for (int q = 0; q < kPfRows / 8; q += 4) {
-        uint16_t in[4][W];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t rr = (q + x) * 8 + warp;  // (few rows: each warp has some)
-          const uint32_t gr = s.c0 + (rr < s.nc ? rr : 0), qi = gr / a.qpk;
-          const uint8_t *src = a.q + int64_t(s.l) * a.q_l + int64_t(s.rs.q0 + qi) * a.q_t +
-                               int64_t(s.h * a.qpk + (gr - qi * a.qpk)) * a.q_h;
-#pragma unroll
-          for (int c = 0; c < W; ++c)
-            in[x][c] = rr < s.nc ? __ldg(reinterpret_cast<const uint16_t *>(src) + lane + 32 * c) : uint16_t(0);
-        }
-        if (uint32_t(q * 8 + warp) >= s.nc) {  // rows that are not there: zeros
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int rr = (q + x) * 8 + warp;
-            if (lane == 0) fcs[rr] = 8.f;
-            if (lane < NG) qss[lane * kPfRows + rr] = 0.f;
-#pragma unroll
-            for (int y = 0; y < 2 * C::SL; ++y)
-              *reinterpret_cast<uint32_t *>(smem + C::q + y * kPfRows * 128 + rr * 128 + 4 * lane) = 0;
-          }
-          continue;
-        }
-        uint64_t w0 = a.c.w0, w1 = a.c.w1;
-        if (a.c.vec_signs) {
-          uint64_t st = a.c.seed + (uint64_t(s.l) * 2 * a.c.heads + s.h) * uint64_t(D / 64) *
-                                       0x9E3779B97F4A7C15ull;
-          w0 = splitmix64(st);
-          if constexpr (D == 128) w1 = splitmix64(st);
-        }
-        float y[4][W];
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-          for (int c = 0; c < W; ++c) {
-            const float u = dtype == KVC_BF16 ? __uint_as_float(uint32_t(in[x][c]) << 16)
-                                              : __half2float(__ushort_as_half(in[x][c]));
-            const uint32_t sg = uint32_t((c < 2 ? w0 : w1) >> (32 * (c & 1) + lane)) & 1u;
-            y[x][c] = __uint_as_float(__float_as_uint(u) ^ (sg << 31));
-          }
-#pragma unroll
-        for (int st = 1; st < 32; st <<= 1)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int c = 0; c < W; ++c) {
-              const float o = __shfl_xor_sync(0xFFFFFFFFu, y[x][c], st);
-              y[x][c] = (lane & st) ? o - y[x][c] : y[x][c] + o;
-            }
-#pragma unroll
-        for (int st = 1; st < W; st <<= 1)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int c = 0; c < W; ++c)
-              if ((c & st) == 0) {
-                const float u = y[x][c], v = y[x][c + st];
-                y[x][c] = u + v;
-                y[x][c + st] = u - v;
-              }
-        float mx[4], gs[4][NG];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          mx[x] = 0.f;
-#pragma unroll
-          for (int g = 0; g < NG; ++g) gs[x][g] = 0.f;
-#pragma unroll
-          for (int c = 0; c < W; ++c) {
-            y[x][c] *= a.scale;
-            mx[x] = fmaxf(mx[x], fabsf(y[x][c]));
-            gs[x][c * 32 / G] += y[x][c];
-          }
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xFFFFFFFFu, mx[x], o));
-#pragma unroll
-            for (int g = 0; g < NG; ++g) gs[x][g] += __shfl_xor_sync(0xFFFFFFFFu, gs[x][g], o);
-          }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int rr = (q + x) * 8 + warp;
-          const int e = int((__float_as_uint(mx[x]) >> 23) & 255u) - 126;
-          const bool fine = mx[x] > 0.f && isfinite(mx[x]) && e > -100;
-          const float es = fine ? __uint_as_float(uint32_t(127 + 14 - e) << 23) : 1.f;
-          if (lane == 0) {
-            fcs[rr] = 8.f / es;
-#pragma unroll
-            for (int g = 0; g < NG; ++g) qss[g * kPfRows + rr] = gs[x][g] * es;
-          }
-          const int i = lane & 7, pos = i < 4 ? 2 * i : 2 * (i - 4) + 1;
-          uint8_t *dst = smem + C::q + rr * 128 + 2 * pos;
-#pragma unroll
-          for (int c = 0; c < W; ++c) {
-            float vh, vl;
-            split_f16(y[x][c] * es, vh, vl);
-            const uint32_t o = (c >> 1) * kPfRows * 128 + (((4 * (c & 1) + (lane >> 3)) ^ (rr & 7)) << 4);
-            *reinterpret_cast<uint16_t *>(dst + o) = __half_as_ushort(__float2half_rn(vh));
-            *reinterpret_cast<uint16_t *>(dst + o + C::QPART) = __half_as_ushort(__float2half_rn(vl));
-          }
-        }
+      // ---- the block's queries, copied at once
+      if (tid == 0) {
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(qcopied, 2 * C::QPART);
+        bulk_g2s(smem + C::q, a.qws + s.unit * C::QB, 2 * C::QPART, qcopied);
       }
-      named_bar_sync(1, kPfSoft);  // every row's factor, sums and parts
+      __syncwarp();
+      const float *qx = reinterpret_cast<const float *>(a.qws + s.unit * C::QB + 2 * C::QPART) + row;
+      const float fc = __ldg(qx);
+      float qsum[NG];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) qsum[g] = __ldg(qx + (1 + g) * kPfRows);
+      int32_t lo = 0, hi = 0;
+      if (uint32_t(row) < s.nc) key_range(a, s.rs, (s.c0 + row) / a.qpk, lo, hi);
+      pf_wait<true>(qcopied, seg & 1u, dead, a.status);
+      ++seg;
+      __syncwarp();
       // this row's hi (first softmax) or lo parts to tensor memory
       if (which == 0 ? C::QH : C::QL) {
         const uint8_t *src = smem + C::q + which * C::QPART + row * 128;
@@ -707,12 +722,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       tm_fence_before();  // (the segment before has been read)
       __syncwarp();
       if (lane == 0) mbar_arrive(qready);
-      const float fc = fcs[row];
-      float qsum[NG];
-#pragma unroll
-      for (int g = 0; g < NG; ++g) qsum[g] = qss[g * kPfRows + row];
-      int32_t lo = 0, hi = 0;
-      if (uint32_t(row) < s.nc) key_range(a, s.rs, (s.c0 + row) / a.qpk, lo, hi);
       // Running state as in kvc_cache_attend.cuh: nm = -m (base 2, and - log2 of the
       // values' common exponent: weights times 2^(a value's e) reach up to 2^15).
       float nm = 0.f, mt = 0.f, thr = -INFINITY, l = 0.f, lw = 0.f, v_most = 0.f;
@@ -907,7 +916,10 @@ cudaError_t cache_prefill_t(int dtype, const CacheAttnArgs &a, int sms, cudaStre
   struct Tag {};
   cudaError_t e = prepare<Tag>(k, C::bytes);
   if (e != cudaSuccess) return e;
-  cache_prefill_prep_kernel<C::NK><<<1, 1024, 0, st>>>(a);
+  static_assert(C::QB == kPfRows * (4 * D + 4 * (1 + C::NG)), "workspace");
+  const uint64_t units = uint64_t(a.c.layers) * a.c.heads * a.max_blocks;
+  cache_prefill_prep_kernel<D, G>
+      <<<unsigned(units * (kPfRows / kPfPrepRows) + 1), kPfPrep, 0, st>>>(a, dtype);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const uint32_t grid = uint32_t(sms) < kCachePrefillCtas ? uint32_t(sms) : kCachePrefillCtas;

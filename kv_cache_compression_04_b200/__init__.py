@@ -510,6 +510,8 @@ class PagedCache:
 
     def __getitem__(self, which) -> "PagedCache":
         if isinstance(which, int):
+            if not -self.pool.shape[0] <= which < self.pool.shape[0]:
+                raise IndexError(f"layer {which} of {self.pool.shape[0]}")
             which = slice(which, which + 1 or None)
         first, _, step = which.indices(self.pool.shape[0])
         if step != 1:
@@ -624,7 +626,7 @@ class PagedCache:
             raise ValueError("stream_buf: expects a contiguous uint8 buffer of nbytes")
         s = self._here(stream, stream_buf, slots)
         n = len(seq_lens)
-        seq, L, D = (C.c_int32 * (n or 1))(*seq_lens), lib(), C.byref(self.desc)
+        seq, L, D = (C.c_int32 * (n or 1))(*map(int, seq_lens)), lib(), C.byref(self.desc)
         ws = self._with_workspace(
             "kvc_cache_load", stream, s, lambda: L.kvc_cache_load_workspace_bytes(D, seq, n),
             lambda at, size: L.kvc_cache_load(stream_buf.data_ptr(), int(nbytes), D, seq, n,

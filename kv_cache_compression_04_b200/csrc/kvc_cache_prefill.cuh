@@ -12,7 +12,11 @@
 //         next product's operand;
 //   O    += P V, V dequantised to fp16 (rounded once, as P is): 128 x D.
 // Floor per 128 x 64 tile pair at d = 128: 3 x 256 cycles of the tensor cores (hi and
-// lo parts, values); the scores' operands come from shared memory and take 1.5 times that.
+// lo parts, values). Measured: 1024 queries x 32 heads over 9216 keys in 284 us (514
+// TFLOP/s of the two products counted once), about 2000 cycles a tile; the tensor cores
+// are active for 0.38 of them, the issuing warp is busy throughout (785 cycles of score
+// products whose lo parts come from shared memory, 200 of values, the rest waits and
+// their latencies). With two groups 343 us, with four 452 us.
 //
 // Warps 0..3 do the even tiles' softmax, 4..7 the odd ones', a thread per row with a
 // maximum, a sum and an output accumulator of its own: the two never wait for each other,
@@ -40,7 +44,7 @@ constexpr int kPfSoft = 256, kPfUnpack = 256, kPfThreads = kPfSoft + kPfUnpack +
 // ones keep 72 and the last four 64 (2 x 128 x (136 + 72) + 128 x 64 = 640 x 96).
 constexpr int kPfSoftRegs = 136, kPfUnpackRegs = 72, kPfIssueRegs = 64;
 constexpr uint32_t kPfStages = 4;
-constexpr uint32_t kPfLead = 3;  // a segment's fixed work, in tiles
+constexpr uint32_t kPfLead = 3;  // a segment's fixed work (queries, record), in tiles
 
 template <int D, int G>
 struct PfCfg {

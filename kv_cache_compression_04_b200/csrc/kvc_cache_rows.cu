@@ -8,6 +8,11 @@
 // and a value's halfwords transposed, include/kvc.h) are what a lane holds:
 // its words are 4 * (head_dim / 32) consecutive bytes of a key row, their
 // halves two consecutive runs of a value row.
+//
+// Bound by instruction issue (the butterfly and codes; 64 tokens x 8 heads are one wave of
+// latency). Measured: 64 tokens written and read back 6.3 us; 4096 tokens x 32 layers, the
+// form for many rows: written in 145 us (0.72 of the copy rate), read in 153 (0.69); loaded
+// in 73 (0.60).
 #include "kvc_cache_rows.cuh"
 
 namespace kvc {
@@ -348,7 +353,8 @@ __global__ void __launch_bounds__(kRowThreads)
   const uint32_t lane = threadIdx.x & 31, p = lane & 3;
   const uint32_t T = uint32_t(a.d.tokens), lkhs = c.layers * 2 * c.heads;
   const uint64_t stream_bytes = ld_u64(in + 56);
-  // 32 tokens of one (layer, kv, head) at a time
+  // 32 tokens of one (layer, kv, head) at a time (two such blocks in step: 5 us slower
+  // in 73)
   const uint32_t tbs = (T + kRowTok - 1) / kRowTok, n = tbs * lkhs;
   for (uint32_t b = blockIdx.x; b < n; b += gridDim.x) {
     const uint32_t lkh = b / tbs, t = (b - lkh * tbs) * kRowTok + (threadIdx.x >> 5) * 8 + (lane >> 2);

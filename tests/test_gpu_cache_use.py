@@ -532,6 +532,10 @@ def test_python_refusals():
                  lambda: c.attend(q[:, :2], tab, lens)):
         with pytest.raises(kvc.KvcError):
             call()
+    for i in (2, -3):
+        with pytest.raises(IndexError):
+            c[i]
+    assert c[-1].desc.first_layer == 1 and c[0:0].desc.layers == 0
     assert status_of(c) == kvc.KVC_OK
 
 

@@ -551,9 +551,10 @@ class PagedCache:
             ws = self._ws[handle] = torch.empty(nbytes(), dtype=torch.uint8, device=self.device)
         return ws
 
-    def _with_workspace(self, where, stream, handle: int, nbytes, call):
-        """call(address, bytes) with a workspace that is large enough; one that is not is
-        refused before anything is enqueued, and replaced."""
+    def _with_workspace(self, where, stream, handle: int, nbytes, call, then=None):
+        """call(address, bytes) with a workspace that is large enough (one that is not is
+        refused before anything is enqueued, and replaced), then(address) before another
+        thread has it."""
         with self._lock:
             ws = self._workspace(stream, handle, nbytes)
             st = call(ws.data_ptr(), ws.numel())
@@ -561,9 +562,10 @@ class PagedCache:
                 self._ws.pop(handle, None)
                 ws = self._workspace(stream, handle, nbytes)
                 st = call(ws.data_ptr(), ws.numel())
+            if st == KVC_OK and then:
+                st = then(ws.data_ptr())
         if st:
             raise KvcError(st, where)
-        return ws
 
     def _dtype(self, name, t):
         kind = self._types.get(t.dtype)
@@ -627,12 +629,11 @@ class PagedCache:
         s = self._here(stream, stream_buf, slots)
         n = len(seq_lens)
         seq, L, D = (C.c_int32 * (n or 1))(*map(int, seq_lens)), lib(), C.byref(self.desc)
-        ws = self._with_workspace(
+        self._with_workspace(
             "kvc_cache_load", stream, s, lambda: L.kvc_cache_load_workspace_bytes(D, seq, n),
             lambda at, size: L.kvc_cache_load(stream_buf.data_ptr(), int(nbytes), D, seq, n,
-                                              slots.data_ptr(), at, size, s))
-        if check:
-            _check(kvc_stream_status(ws.data_ptr(), s), "kvc_cache_load (device)")
+                                              slots.data_ptr(), at, size, s),
+            (lambda at: kvc_stream_status(at, s)) if check else None)
 
     def attend(self, q, page_table, seq_lens, q_starts=None, max_q: int = 1, out=None, lse=None,
                scale: float | None = None, causal: bool = True, window: int = 0, stream=None):

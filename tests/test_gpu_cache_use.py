@@ -499,7 +499,19 @@ def test_other_streams_threads_and_repeats():
     def work(i):
         got[i] = [c.attend(qs[x % 3], tab, lens, q_starts=st[x % 3], max_q=qs[x % 3].shape[1]) for x in range(30)]
 
-    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    kv = torch.randn(1, 2, H, 16, d, device="cuda").to(torch.bfloat16)
+    buf, nbytes, _ = stream_of(kv, g, 11, 0, 0, 0)
+    free = torch.arange(128 * 16, 129 * 16, device="cuda")  # a page of no request
+
+    def load():
+        try:
+            for _ in range(30):
+                c.load(buf, nbytes, free, [16], check=True)
+            got["load"] = True
+        except kvc.KvcError as e:
+            got["load"] = e
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)] + [threading.Thread(target=load)]
     for t in threads:
         t.start()
     for t in threads:
@@ -507,6 +519,7 @@ def test_other_streams_threads_and_repeats():
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(o, want[x % 3]) for x, o in enumerate(got[i]))
+    assert got["load"] is True
     c.check()
 
 

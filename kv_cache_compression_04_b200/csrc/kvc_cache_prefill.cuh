@@ -12,18 +12,18 @@
 //         next product's operand;
 //   O    += P V, V dequantised to fp16 (rounded once, as P is): 128 x D.
 // Floor per 128 x 64 tile pair at d = 128: 3 x 256 cycles of the tensor cores (hi and
-// lo parts, values). Measured: 1024 queries x 32 heads over 9216 keys in 284 us (514
-// TFLOP/s of the two products counted once), about 2000 cycles a tile; the tensor cores
-// are active for 0.38 of them, the issuing warp is busy throughout (785 cycles of score
-// products whose lo parts come from shared memory, 200 of values, the rest waits and
-// their latencies). With two groups 343 us, with four 452 us.
+// lo parts, values). Measured: 1024 queries x 32 heads over 9216 keys in 270 us (540
+// TFLOP/s of the two products counted once), about 1900 cycles a tile, of which the
+// tensor cores are active for 768. A softmax takes 3100 of its two tiles' 3800 (two
+// softmax and two unpacking warps share an SM quarter's issue), unpacking 2900. With two
+// groups 343 us, with four 464 us (two tiles' scores fit, and twice the fused multiplies).
 //
 // Warps 0..3 do the even tiles' softmax, 4..7 the odd ones', a thread per row with a
 // maximum, a sum and an output accumulator of its own: the two never wait for each other,
 // and one's exponentials run beside the other's products. Their results meet at a
 // segment's end. Warps 8..11 unpack the even tiles, 12..15 the odd ones, up to four
-// tiles ahead. Warp 16 starts the products: a start waits while the tensor cores' queue
-// is full, which would hold up a softmax warp.
+// tiles ahead. Warps 16 and 17 start the products (PfIssue): from a softmax warp, a start
+// that waits for the tensor cores' queue held up the whole block.
 // Work is shared out as in kvc_cache_attend.cuh, a share per CTA (one per SM).
 //
 // Shared memory, 128-byte swizzle (16-byte piece c of row r at c ^ (r & 7)):
@@ -161,6 +161,13 @@ __device__ __forceinline__ void tm_commit(uint64_t *bar) {
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
           smem_u32(bar))
       : "memory");
+}
+
+// The largest of three, as fmaxf: a NaN only if all are.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // Bounded wait for the phase with the given parity; a wait that runs out marks the
@@ -543,89 +550,135 @@ __device__ __forceinline__ void pf_unpack(const CacheAttnArgs &a, uint8_t *smem,
   }
 }
 
-// The issuing warp: every tile's products, QK 0 .. QK NS - 1, then PV i, QK i + NS, whose
-// scores replace tile i's weights (the tensor cores take products one after the other).
-// Its time is a tile's: places and phases are counted on, not divided out (a poll with
-// these divisions took 500 cycles).
+// Starting products. A start takes as long as its products where the tensor cores' queue
+// is full, and a wait some hundred cycles. With three tiles' scores one warp starts scores
+// and one values (one for both was busy for 2000 cycles a tile, which bounded the kernel:
+// 284 us against 268 for 1024 queries over 9216 keys). Products of two threads are not
+// ordered: there a tile's scores wait until the values of the tile NS before, whose weights
+// they replace, are done. With two tiles' scores that wait costs more than it gives (343 us
+// with one warp, 356 with two, at two groups): one warp starts values i, then scores i + 2.
 template <int D, int G>
-__device__ __forceinline__ void pf_issue(const CacheAttnArgs &a, uint8_t *smem, uint32_t tm,
-                                         uint64_t f, uint64_t f_end) {
+struct PfIssue {
   using C = PfCfg<D, G>;
-  constexpr int NG = C::NG, NK = C::NK, SG = G / 16;  // (16-channel steps of a group)
-  constexpr uint32_t NS = C::NS, ST = kPfStages;
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::bars), *pv = full + ST;
-  uint64_t *sready = pv + ST, *pready = sready + NS, *qready = pready + NS;
-  volatile uint32_t *dead = reinterpret_cast<uint32_t *>(smem + C::ctl) + 1;
-  const uint32_t q_s = smem_u32(smem + C::q), k_s = smem_u32(smem + C::k), v_s = smem_u32(smem + C::v);
-  // scores of the tile in stage st to place sb
-  auto scores = [&](uint32_t st, uint32_t phase, uint32_t sb) {
-    pf_wait(full + st, phase, dead, a.status);
+  static constexpr uint32_t NS = C::NS, ST = kPfStages;
+  uint32_t tm, q_s, k_s, v_s, *status;
+  uint64_t *full, *pv, *sready, *pready, *qready;
+  volatile uint32_t *dead;
+  __device__ __forceinline__ PfIssue(const CacheAttnArgs &a, uint8_t *smem, uint32_t tm_)
+      : tm(tm_), q_s(smem_u32(smem + C::q)), k_s(smem_u32(smem + C::k)), v_s(smem_u32(smem + C::v)),
+        status(a.status) {
+    full = reinterpret_cast<uint64_t *>(smem + C::bars);
+    pv = full + ST;
+    sready = pv + ST;
+    pready = sready + NS;
+    qready = pready + NS;
+    dead = reinterpret_cast<uint32_t *>(smem + C::ctl) + 1;
+  }
+  __device__ __forceinline__ void wait(uint64_t *bar, uint32_t phase) const {
+    pf_wait(bar, phase, dead, status);
+  }
+  // Scores of the tile in stage st to place sb.
+  __device__ __forceinline__ void scores(uint32_t st, uint32_t sb) const {
+    constexpr int SG = G / 16;  // (16-channel steps of a group)
     tm_fence_after();
     __syncwarp();
     const uint64_t dq = tm_desc(q_s, 16, 1024), dk = tm_desc(k_s + st * C::KBUF, 16, 1024);
     const uint32_t ts = tm + C::tS + sb * C::SW;
     if (tm_elect()) {
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
+      for (int g = 0; g < C::NG; ++g)
 #pragma unroll
         for (int x = 0; x < 2 * SG; ++x) {  // hi parts, then lo
           const int c = g * SG + x % SG, o = (c & 3) * 2;
-          const uint64_t k = dk + (((c >> 2) * NK * 128) >> 4) + o;
+          const uint64_t k = dk + (((c >> 2) * C::NK * 128) >> 4) + o;
           if (x < SG ? C::QH : C::QL)
-            tm_mma_ts(ts + g * NK, tm + C::tQ + (x / SG) * (D / 2) + c * 8, k, tm_idesc(NK, false), x != 0);
+            tm_mma_ts(ts + g * C::NK, tm + C::tQ + (x / SG) * (D / 2) + c * 8, k, tm_idesc(C::NK, false),
+                      x != 0);
           else
-            tm_mma(ts + g * NK, dq + (((x / SG) * C::QPART + (c >> 2) * kPfRows * 128) >> 4) + o, k,
-                   tm_idesc(NK, false), x != 0);
+            tm_mma(ts + g * C::NK, dq + (((x / SG) * C::QPART + (c >> 2) * kPfRows * 128) >> 4) + o, k,
+                   tm_idesc(C::NK, false), x != 0);
         }
       tm_commit(sready + sb);
     }
     __syncwarp();
-  };
-  uint32_t j0 = 0;
-  for (uint32_t seg = 0; f < f_end;) {
+  }
+  // Weights at place sb times the values of stage st, for softmax `odd`.
+  __device__ __forceinline__ void values(uint32_t st, uint32_t sb, uint32_t odd, bool add) const {
+    tm_fence_after();
+    __syncwarp();
+    const uint64_t dv = tm_desc(v_s + st * C::KBUF, C::NK * 128, 1024);
+    const uint32_t ts = tm + C::tS + sb * C::SW, to = tm + C::tO + odd * D;
+    if (tm_elect()) {
+#pragma unroll
+      for (int x = 0; x < C::NK / 16; ++x)
+        tm_mma_ts(to, ts + x * 8, dv + x * 128, tm_idesc(D, true), add || x != 0);
+      tm_commit(pv + st);
+    }
+    __syncwarp();
+  }
+};
+// A place among N and the phase it is in, counted on (a division per tile is dear here).
+template <uint32_t N>
+struct PfPlace {
+  uint32_t at = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    phase ^= at == N - 1 ? 1u : 0u;
+    at = at == N - 1 ? 0 : at + 1;
+  }
+};
+
+// which: 0 scores (and values, with two tiles' scores), 1 values.
+template <int D, int G>
+__device__ __forceinline__ void pf_issue(const CacheAttnArgs &a, uint8_t *smem, uint32_t tm,
+                                         uint32_t which, uint64_t f, uint64_t f_end) {
+  using C = PfCfg<D, G>;
+  constexpr uint32_t NS = C::NS, ST = kPfStages;
+  const PfIssue<D, G> p(a, smem, tm);
+  PfPlace<ST> ks, vs;  // stages of the next scores and values
+  PfPlace<NS> sb, wb;  // places of the next scores and weights
+  uint32_t before = 0, seg = 0, odd = 0;
+  if (NS == 2 && which == 1) return;
+  while (f < f_end) {
     const PfSegment s = pf_segment_at(a, f_end, f);
     if (s.tiles == 0) continue;
     const uint32_t tiles = tm_uniform(s.tiles);
-    // tile i's place and its phase; the stage and its phase of tile i, of the next scores
-    uint32_t sb = tm_uniform(j0 % NS), sp = tm_uniform((j0 / NS) & 1u), odd = tm_uniform(j0 & 1u);
-    uint32_t st = tm_uniform(j0 % ST), kt = st, kp = tm_uniform((j0 / ST) & 1u);
-    pf_wait(qready, seg & 1u, dead, a.status);
-    tm_fence_after();
-    __syncwarp();
-    auto next_keys = [&]() {
-      kp ^= kt == ST - 1 ? 1u : 0u;
-      kt = kt == ST - 1 ? 0 : kt + 1;
+    if (which == 0) {
+      p.wait(p.qready, seg & 1u);
+      ++seg;
+    }
+    auto scores = [&]() {
+      p.wait(p.full + ks.at, ks.phase);
+      p.scores(ks.at, sb.at);
+      ks.next();
+      sb.next();
     };
-    uint32_t place = sb;
-    for (uint32_t q = 0; q < NS && q < tiles; ++q) {
-      scores(kt, kp, place);
-      next_keys();
-      place = place == NS - 1 ? 0 : place + 1;
-    }
-    for (uint32_t i = 0; i < tiles; ++i) {
-      pf_wait(pready + sb, sp, dead, a.status);
-      tm_fence_after();
-      __syncwarp();
-      const uint64_t dv = tm_desc(v_s + st * C::KBUF, NK * 128, 1024);
-      const uint32_t ts = tm + C::tS + sb * C::SW, to = tm + C::tO + odd * D;
-      if (tm_elect()) {
-#pragma unroll
-        for (int x = 0; x < NK / 16; ++x)
-          tm_mma_ts(to, ts + x * 8, dv + x * 128, tm_idesc(D, true), i > 1 || x != 0);
-        tm_commit(pv + st);
-      }
-      __syncwarp();
-      if (i + NS < tiles) {
-        scores(kt, kp, sb);
-        next_keys();
-      }
-      sp ^= sb == NS - 1 ? 1u : 0u;
-      sb = sb == NS - 1 ? 0 : sb + 1;
-      st = st == ST - 1 ? 0 : st + 1;
+    auto values = [&](uint32_t i) {
+      p.wait(p.pready + wb.at, wb.phase);
+      p.values(vs.at, wb.at, odd, i > 1);
+      vs.next();
+      wb.next();
       odd ^= 1u;
+    };
+    if constexpr (NS == 2) {
+      scores();
+      if (tiles > 1) scores();
+      for (uint32_t i = 0; i < tiles; ++i) {
+        values(i);
+        if (i + 2 < tiles) scores();
+      }
+    } else if (which == 0) {
+      for (uint32_t i = 0; i < tiles; ++i) {
+        if (before == NS) {  // (vs: the stage of the tile NS before)
+          p.wait(p.pv + vs.at, vs.phase);
+          vs.next();
+        } else {
+          ++before;
+        }
+        scores();
+      }
+    } else {
+      for (uint32_t i = 0; i < tiles; ++i) values(i);
     }
-    j0 += tiles;
-    ++seg;
   }
 }
 
@@ -674,7 +727,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 
   if (warp >= (kPfSoft + kPfUnpack) / 32) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPfIssueRegs));
-    if (warp == (kPfSoft + kPfUnpack) / 32) pf_issue<D, G>(a, smem, tm_uniform(tm), f, f_end);
+    const uint32_t which = uint32_t(warp) - (kPfSoft + kPfUnpack) / 32;
+    if (which == 0) pf_issue<D, G>(a, smem, tm_uniform(tm), 0, f, f_end);
+    if (which == 1) pf_issue<D, G>(a, smem, tm_uniform(tm), 1, f, f_end);
   } else if (warp >= kPfSoft / 32) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPfUnpackRegs));
     pf_unpack<D, G>(a, smem, uint32_t(warp >> 2) & 1u, f, f_end);
@@ -775,8 +830,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         float tops[4] = {sc[0], sc[1], sc[2], sc[3]};
 #pragma unroll
-        for (int x = 4; x < NK; ++x) tops[x & 3] = fmaxf(tops[x & 3], sc[x]);
-        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+        for (int x = 4; x + 4 < NK; x += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) tops[y] = max3(tops[y], sc[x + y], sc[x + y + 4]);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) tops[y] = fmaxf(tops[y], sc[NK - 4 + y]);
+        const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
         const float4 wm = *reinterpret_cast<const float4 *>(smem + C::wmax + buf * 16);
         const float vm = fmaxf(fmaxf(wm.x, wm.y), fmaxf(wm.z, wm.w));
         if (__any_sync(0xFFFFFFFFu, top > thr) || vm > v_most) {

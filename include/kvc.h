@@ -506,8 +506,9 @@ uint64_t kvc_cache_stream_seed(const kvc_cache_desc *cache);
  * its row of the page table) sets KVC_ERR_CORRUPT and its rows are left as they
  * were (where q_starts decrease, the other requests' rows are unspecified); a
  * page outside the pool sets it too and the page's tokens are left out.
- * Three kernels. max_q and q_per_kv choose the form: up to 48 query rows
- * (max_q * q_per_kv) are taken 4, 8 or 16 at a time, more in blocks of 128. */
+ * Three kernels. max_q and q_per_kv choose the form: up to 32 query rows
+ * (max_q * q_per_kv; 48 at head_dim 64) are taken 4, 8 or 16 at a time, more in
+ * blocks of 128. */
 #define KVC_CACHE_MAX_Q_PER_KV 64
 typedef struct {
   int32_t dtype;              /* KVC_BF16 or KVC_FP16, of q and out */

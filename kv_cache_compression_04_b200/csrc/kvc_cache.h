@@ -74,15 +74,14 @@ struct CacheAttnArgs {
 };
 
 // Query rows of one unit of the attention: a request's (queries x query heads per kv
-// head) rounded up to 4, 8 or 16; blocks of 16 (warp products) up to kCacheFewRows, of 128
+// head) rounded up to 4, 8 or 16; blocks of 16 (warp products) for a few more, of 128
 // (tcgen05) above. A block of 16 reads the keys once more, one of 128 rows takes as long
-// for 20 as for 128: 16 requests x 8 heads, blocks of 16 against of 128, in us, 32 / 48 /
-// 64 rows: 4096 keys 75 / 105 / 136 against 84 / 90 / 94 (d 128), 47 / 66 / 81 against 74 /
-// 78 / 81 (d 64); 1024 keys 33 / 43 / 49 against 44 / 48 / 53, 25 / 32 / 35 against 38 / 42 /
-// 45.
-constexpr uint64_t kCacheFewRows = 48;
-inline int cache_cols(uint64_t rows) {
-  return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= kCacheFewRows ? 16 : 128;
+// for 20 as for 128. 16 requests x 8 heads, blocks of 16 against of 128, in us, 32 / 48 / 64
+// rows: 4096 keys 78 / 104 / 128 against 84 / 89 / 93 (d 128), 47 / 66 / 81 against 67 / 70 /
+// 71 (d 64); 1024 keys 33 / 44 / 50 against 41 / 45 / 46, 25 / 32 / 35 against 35 / 38 / 39.
+inline uint64_t cache_few_rows(int d) { return d == 128 ? 32 : 48; }
+inline int cache_cols(uint64_t rows, int d) {
+  return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= cache_few_rows(d) ? 16 : 128;
 }
 // A unit's query fragments in the workspace, bytes: 16-bit hi and lo parts, then
 // factors and sums.

@@ -151,7 +151,7 @@ kvc_status check_attn(const kvc_cache_desc *cache, const kvc_cache_attn *t, Cach
     return KVC_ERR_UNSUPPORTED;
   if (!t->q_starts && t->q_tokens < t->n_requests) return KVC_ERR_INVALID_ARG;
   const uint64_t heads = uint64_t(cache->kv_heads), qpk = uint64_t(t->q_per_kv);
-  const uint64_t rows = uint64_t(t->max_q) * qpk, cols = uint64_t(cache_cols(rows));
+  const uint64_t rows = uint64_t(t->max_q) * qpk, cols = uint64_t(cache_cols(rows, cache->head_dim));
   const uint64_t reqs = uint64_t(t->n_requests), lh = uint64_t(cache->layers) * heads;
   w.blocks = cols > 16 ? uint64_t(t->q_tokens) * qpk / cols + reqs : reqs * ((rows + cols - 1) / cols);
   const uint64_t units = lh * w.blocks;
@@ -323,7 +323,7 @@ kvc_status kvc_cache_attend(const kvc_cache_desc *cache, const kvc_cache_attn *t
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const int g = cache->group_size;
   cudaError_t e;
-  if (uint64_t(t->max_q) * uint64_t(t->q_per_kv) > kCacheFewRows)
+  if (uint64_t(t->max_q) * uint64_t(t->q_per_kv) > cache_few_rows(cache->head_dim))
     e = cache->head_dim == 128 ? launch_cache_prefill_d128(g, t->dtype, a, sms, cs)
                                : launch_cache_prefill_d64(g, t->dtype, a, sms, cs);
   else

@@ -29,7 +29,7 @@
 // products.
 //
 // Few query rows (queries x query heads per kv head) of a request, 16 at a time; many are
-// kvc_cache_prefill.cuh's (kCacheFewRows).
+// kvc_cache_prefill.cuh's (cache_few_rows).
 //
 // Work. A unit is (layer, kv head, block of a request's rows); its keys are chunks of 32
 // tokens (two tiles). All units' chunks in a row, each unit with

@@ -164,7 +164,7 @@ def test_attention_workspace():
     """One record per unit and per warp of the launch (few rows) or CTA (blocks of 128), of
     cols x (4 + head_dim) floats, and the prefixes, shapes, fragments or block numbers."""
     for max_q, qpk, cols, blocks, extra in ((1, 4, 4, 3, 2560), (2, 4, 8, 3, 2560), (1, 9, 16, 3, 2560),
-                                            (12, 4, 16, 9, 2560), (13, 4, 128, 3 + 39 * 4 // 128, 160)):
+                                            (8, 4, 16, 6, 2560), (9, 4, 128, 3 + 27 * 4 // 128, 160)):
         t = attn(max_q=max_q, q_per_kv=qpk, q_tokens=3 * max_q, q_starts=FAKE)
         units = 2 * 8 * blocks
         rec = (units + extra) * cols * 132 * 4

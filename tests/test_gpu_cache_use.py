@@ -287,8 +287,8 @@ def test_high_offsets():
 # ------------------------------------------------------------ attention --
 @pytest.mark.parametrize("d,g", KINDS)
 @pytest.mark.parametrize("qpk,asked,causal,window", [
-    (4, 5, True, 0), (16, 3, True, 21), (12, 4, False, 0),   # 20, 48, 48 rows: blocks of 16
-    (7, 7, True, 0), (64, 1, True, 0), (3, 90, True, 33), (8, 33, False, 0)])  # 49 .. 270: of 128
+    (4, 5, True, 0), (8, 4, True, 21), (16, 3, True, 21), (12, 4, False, 0),  # 20 .. 48 rows
+    (7, 7, True, 0), (64, 1, True, 0), (3, 90, True, 33), (8, 33, False, 0)])  # 49 .. 270: blocks of 128
 def test_attend_many_rows(d, g, qpk, asked, causal, window):
     lens = [170, 1, 64, 65, 300]
     c = make(d, g, 1, 2, 64, 16, signs=1)

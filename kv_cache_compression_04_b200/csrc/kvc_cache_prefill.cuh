@@ -12,11 +12,12 @@
 //         next product's operand;
 //   O    += P V, V dequantised to fp16 (rounded once, as P is): 128 x D.
 // Floor per 128 x 64 tile pair at d = 128: 3 x 256 cycles of the tensor cores (hi and
-// lo parts, values). Measured: 1024 queries x 32 heads over 9216 keys in 270 us (540
-// TFLOP/s of the two products counted once), about 1900 cycles a tile, of which the
-// tensor cores are active for 768. A softmax takes 3100 of its two tiles' 3800 (two
-// softmax and two unpacking warps share an SM quarter's issue), unpacking 2900. With two
-// groups 343 us, with four 464 us (two tiles' scores fit, and twice the fused multiplies).
+// lo parts, values). Measured: 1024 queries x 32 heads over 9216 keys in 255 us (574
+// TFLOP/s of the two products counted once), about 1750 cycles a tile, of which the
+// tensor cores are active for 768. A softmax works for most of its two tiles' time (two
+// softmax and two unpacking warps share an SM quarter's issue, 58% of it used), and
+// shared memory serves 850 wavefronts and the products' operands a tile. With two groups
+// 316 us, with four 447 us (two tiles' scores fit, and more fused multiplies).
 //
 // Warps 0..3 do the even tiles' softmax, 4..7 the odd ones', a thread per row with a
 // maximum, a sum and an output accumulator of its own: the two never wait for each other,
@@ -408,6 +409,7 @@ __device__ __forceinline__ void pf_unpack(const CacheAttnArgs &a, uint8_t *smem,
   constexpr int NG = C::NG, NK = C::NK, W = C::W, RX = Raw::RX;
   const uint32_t t = threadIdx.x & 127, lane = t & 31, warp = t >> 5, p = t & 3;
   const uint32_t r0 = 8 * warp + 4 * ((t >> 2) & 1) + ((t >> 3) & 3);
+  const uint32_t flip = W == 4 ? 2 * (p >> 1) + ((t >> 2) & 1) : (t >> 2) & 1;
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::bars), *pv = full + kPfStages;
   volatile uint32_t *dead = reinterpret_cast<uint32_t *>(smem + C::ctl) + 1;
   uint32_t j0 = 0;  // tiles before the segment
@@ -503,11 +505,32 @@ __device__ __forceinline__ void pf_unpack(const CacheAttnArgs &a, uint8_t *smem,
           sv[g] = half_lo(m) * inv;
           zv[g] = zero8(m) * inv;
         }
+        // a lane's words in an order of its own (q ^ flip): in step, eight lanes' pieces
+        // would meet in two columns of the banks (17 of 43 million wavefronts)
+        uint32_t vw[W];
+#pragma unroll
+        for (int q = 0; q < W; ++q) vw[q] = w.v[x][q];
+        auto swap_if = [](bool yes, auto &a, auto &b) {
+          const auto c = yes ? b : a;
+          b = yes ? a : b;
+          a = c;
+        };
+#pragma unroll
+        for (int q = 0; q < W; q += 2) swap_if(flip & 1, vw[q], vw[q + 1]);
+        if constexpr (W == 4) {
+          swap_if(flip & 2, vw[0], vw[2]);
+          swap_if(flip & 2, vw[1], vw[3]);
+#pragma unroll
+          for (int g = 0; g < NG / 2; ++g) {  // the groups of words q and q ^ 1
+            swap_if(flip & 1, sv[g], sv[g + NG / 2]);
+            swap_if(flip & 1, zv[g], zv[g + NG / 2]);
+          }
+        }
 #pragma unroll
         for (int q = 0; q < W; ++q) {
-          const int wj = W * int(p) + q;  // stored word: halves of 32-channel blocks a, a + 1
+          const uint32_t wj = W * p + (q ^ flip);  // stored word: halves of 32-channel blocks a, a + 1
           const int ga = ((2 * q) % W) * 32 / G, gb = ((2 * q) % W + 1) * 32 / G;
-          const uint32_t s2 = f16x2(sv[ga], sv[gb]), z2 = f16x2(zv[ga], zv[gb]), u = w.v[x][q];
+          const uint32_t s2 = f16x2(sv[ga], sv[gb]), z2 = f16x2(zv[ga], zv[gb]), u = vw[q];
           auto deq = [&](uint32_t n) {
             uint32_t d;
             asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(n), "r"(s2), "r"(z2));

@@ -539,16 +539,17 @@ class PagedCache:
         return stream.cuda_stream
 
     def _workspace(self, stream, handle: int, nbytes):
-        """The stream's workspace if it has nbytes() (called where that has to be known)."""
+        """The stream's workspace if it has nbytes() (called where that has to be known; 0 for
+        arguments that the call then refuses, which no null pointer may hide)."""
         import torch
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self._workspace(None, handle, nbytes)
         if torch._C._cuda_isCurrentStreamCapturing():  # a graph's own, from its memory pool
-            return torch.empty(nbytes(), dtype=torch.uint8, device=self.device)
+            return torch.empty(max(1, nbytes()), dtype=torch.uint8, device=self.device)
         ws = self._ws.get(handle)
         if ws is None:
-            ws = self._ws[handle] = torch.empty(nbytes(), dtype=torch.uint8, device=self.device)
+            ws = self._ws[handle] = torch.empty(max(1, nbytes()), dtype=torch.uint8, device=self.device)
         return ws
 
     def _with_workspace(self, where, stream, handle: int, nbytes, call, then=None):
@@ -676,8 +677,8 @@ class PagedCache:
         except (struct.error, OverflowError) as e:
             raise ValueError(f"max_q, window, scale: {e}") from None
         self._with_workspace(
-            "kvc_cache_attend", stream, s, lambda: max(1, lib().kvc_cache_attend_workspace_bytes(
-                C.byref(self.desc), C.cast(t, C.POINTER(kvc_cache_attn)))),
+            "kvc_cache_attend", stream, s, lambda: lib().kvc_cache_attend_workspace_bytes(
+                C.byref(self.desc), C.cast(t, C.POINTER(kvc_cache_attn))),
             lambda at, size: self._attend(self._desc, t, at, size, self._status, s))
         return out
 

@@ -1,0 +1,55 @@
+"""PagedCache's own checks without a GPU: a cache over CPU memory whose calls end where
+something would be enqueued."""
+import contextlib
+
+import pytest
+import torch
+
+import kv_cache_compression_04_b200 as kvc
+from kv_cache_compression_04_b200 import build
+
+ENQUEUED = kvc.KVC_ERR_CUDA  # what a call that passes its checks ends with here
+
+
+class HostCache(kvc.PagedCache):
+    """A cache whose pool, status word and workspaces are CPU memory."""
+
+    def __init__(self, layers=1, heads=2, d=128, pages=4, page=16, group=64):
+        self.status = torch.zeros(1, dtype=torch.int32)
+        self._ws, self._lock, self._calls = {}, kvc.threading.Lock(), (None, None, None, {})
+        desc = kvc.kvc_cache_desc(layers, heads, d, 4, group, 0, 0, 0, 3, page, 0, pages)
+        block = kvc.kvc_cache_block_bytes(desc)
+        self._set(desc, torch.zeros(layers, pages, 2, heads, block, dtype=torch.uint8))
+
+    def _here(self, stream, *tensors):
+        return 0
+
+
+@pytest.fixture(autouse=True)
+def no_gpu(monkeypatch):
+    if torch.cuda.is_available():
+        pytest.skip("the accepted calls would be enqueued on CPU pointers")
+    build.build()
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+
+
+def load(c, lens, nbytes=64):
+    n = sum(lens)
+    c.load(torch.zeros(64, dtype=torch.uint8), nbytes, torch.zeros(n, dtype=torch.int64), lens)
+
+
+def status(call):
+    with pytest.raises(kvc.KvcError) as e:
+        call()
+    return e.value.status
+
+
+@pytest.mark.parametrize("refused", [[1] * 1025, [3, -1], [2 ** 31 - 1, 1 - 2 ** 31]])
+def test_a_refused_load_leaves_the_stream_usable(refused):
+    """The first call on a stream: nothing of it is kept."""
+    c = HostCache()
+    assert status(lambda: load(c, refused)) == kvc.KVC_ERR_INVALID_ARG
+    assert status(lambda: load(c, [5])) == ENQUEUED
+    assert status(lambda: load(c, refused)) == kvc.KVC_ERR_INVALID_ARG
+    assert status(lambda: load(c, [500])) == ENQUEUED

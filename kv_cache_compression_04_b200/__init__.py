@@ -624,7 +624,7 @@ class PagedCache:
             raise ValueError("slots: expects a contiguous int64 vector")
         if slots.shape[0] != sum(seq_lens):
             raise ValueError(f"{slots.shape[0]} slots for {sum(seq_lens)} tokens")
-        if stream_buf.dtype != torch.uint8 or stream_buf.numel() < int(nbytes) or \
+        if stream_buf.dtype != torch.uint8 or not 0 <= int(nbytes) <= stream_buf.numel() or \
                 not stream_buf.is_contiguous():
             raise ValueError("stream_buf: expects a contiguous uint8 buffer of nbytes")
         s = self._here(stream, stream_buf, slots)

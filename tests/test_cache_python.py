@@ -53,3 +53,10 @@ def test_a_refused_load_leaves_the_stream_usable(refused):
     assert status(lambda: load(c, [5])) == ENQUEUED
     assert status(lambda: load(c, refused)) == kvc.KVC_ERR_INVALID_ARG
     assert status(lambda: load(c, [500])) == ENQUEUED
+
+
+@pytest.mark.parametrize("nbytes", [-1, -2 ** 63, 65, 2 ** 64])
+def test_load_refuses_a_size_that_the_buffer_does_not_have(nbytes):
+    """A negative one would reach the library as a size near 2^64."""
+    with pytest.raises(ValueError):
+        load(HostCache(), [5], nbytes)

@@ -469,7 +469,7 @@ kvc_status kvc_cache_read(const kvc_cache_desc *cache, const kvc_cache_rows *row
  * vectors of the stream's token t (requests concatenated in order, as
  * kvc_compress codes them) go to slots[t] (DEVICE, [sum of seq_lens]; negative:
  * the token is skipped). The stream must describe layers x kv_heads x
- * head_dim vectors of as many requests and tokens, 4-bit ASYM or SYM codes of
+ * head_dim vectors of as many requests, each of its seq_lens, 4-bit ASYM or SYM codes of
  * this group size, the same sign mode and the same diagonals (with per-vector diagonals
  * and first_layer > 0: a stream of those layers alone whose seed is the one
  * whose diagonal 0 is theirs, see kvc_cache_stream_seed), and store its code

@@ -41,7 +41,10 @@ struct RowArgs {
 struct LoadArgs {
   DecArgs d;  // header fields, status and the expanded meta chunks
   uint32_t group;
+  uint32_t table_fits;    // 1: in_bytes reach past the token table
+  uint64_t tokens_at;     // of the token table, for the chunks that the caller's numbers give
   const int64_t *slots;
+  uint32_t lens[KVC_MAX_REQUESTS];
 };
 
 // kvc_cache_attend. Strides in bytes.

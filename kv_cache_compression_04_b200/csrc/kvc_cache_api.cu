@@ -255,6 +255,10 @@ kvc_status kvc_cache_load(const void *in, size_t in_bytes, const kvc_cache_desc 
   a.d.ws_meta = static_cast<uint8_t *>(workspace) + kWsCtl;
   a.d.ws_meta_chunks = uint32_t(s.meta_chunks);
   a.group = uint32_t(cache->group_size);
+  const uint64_t code_chunks = (s.vectors * uint64_t(cache->head_dim / 2) + kChunk - 1) / kChunk;
+  a.tokens_at = kHeader + 8 * (code_chunks + s.meta_chunks);
+  a.table_fits = a.tokens_at + 4 * uint64_t(n_requests) <= in_bytes ? 1u : 0u;
+  for (int32_t i = 0; i < n_requests; ++i) a.lens[i] = uint32_t(seq_lens[i]);
   a.slots = slots;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(workspace, 0, kWsCtl, cs) != cudaSuccess) return KVC_ERR_CUDA;

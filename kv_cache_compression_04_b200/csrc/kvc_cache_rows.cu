@@ -333,21 +333,27 @@ template <int D, int G>
 __global__ void __launch_bounds__(kRowThreads)
     cache_load_kernel(const __grid_constant__ CachePool c, const __grid_constant__ LoadArgs a) {
   using C = Cfg<D, 4, G>;
-  __shared__ uint32_t ok_s;
   __shared__ uint64_t base_s;
   grid_dependency_wait();  // the meta expansion
   const uint8_t *in = a.d.in, *table = in + kHeader;
+  // A thread checks the header; all warps but its own compare the requests' lengths at the
+  // same time, where the table is if the header is right.
+  bool bad = false;
   if (threadIdx.x == 0) {
     const StreamHdr h = parse_header<D>(a.d);
     bool ok = h.ok && h.bits == 4 && h.group == a.group && h.quant <= 1 && !h.code_elim &&
               h.vec_signs == c.vec_signs && h.seed == c.seed &&
               h.data_base + uint64_t(a.d.V) * C::CB <= h.stream_bytes;
-    ok_s = ok;
+    bad = !ok;
     base_s = h.data_base;
-    if (!ok) set_status(a.d.status, KVC_ERR_CORRUPT);
+  } else if (threadIdx.x >= 32 && a.table_fits) {
+    for (uint32_t r = threadIdx.x - 32; r < a.d.n_req; r += kRowThreads - 32)
+      bad |= ld_u32(in + a.tokens_at + 4 * r) != a.lens[r];
   }
-  __syncthreads();
-  if (!ok_s) return;
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) set_status(a.d.status, KVC_ERR_CORRUPT);
+    return;
+  }
   const uint64_t base = base_s, code_bytes = uint64_t(a.d.V) * C::CB;
   const uint64_t n_code = (code_bytes + kChunk - 1) / kChunk;
   const uint32_t lane = threadIdx.x & 31, p = lane & 3;

@@ -1,0 +1,57 @@
+"""The paged 4-bit cache on the GPU where its calls could go wrong unseen: streams whose
+requests are cut elsewhere, errors of a load that nobody waits for, values that no query
+should see by their size, and the largest lengths."""
+import numpy as np
+import pytest
+import torch
+
+import cache_ref as ref
+import kv_cache_compression_04_b200 as kvc
+from test_gpu_cache import KINDS, make, rows, slots_for
+from test_gpu_cache_use import CORRUPT, cache_values, close, dev, narrow_meta, status_of, stream_of
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- load --
+def paged_stream(lens, L, H, d, g, seed):
+    """A stream of several requests, and what it decodes to: rows [L, 2, H, tokens, d]."""
+    page, T = 16, sum(lens)
+    per = [-(-n // page) for n in lens]
+    pool = torch.randn(L, sum(per) + 1, 2, H, page, d, device="cuda").to(torch.bfloat16)
+    table = torch.zeros(len(lens), max(per + [1]), dtype=torch.int32)
+    at, rows = 0, []
+    for r, n in enumerate(per):
+        table[r, :n] = torch.arange(at, at + n)
+        t = torch.arange(lens[r])
+        rows.append((at + t // page) * page + t % page)
+        at += n
+    table = table.cuda()
+    codec = kvc.Codec(4, g, seed)
+    out, ws, n = codec.compress(kvc.paged_desc(pool, table, lens))
+    back = torch.zeros_like(pool)
+    codec.decompress(out, int(n.item()), kvc.paged_desc(back, table, lens), ws)
+    rows = torch.cat(rows).cuda()
+    x = back.permute(0, 2, 3, 1, 4, 5).reshape(L, 2, H, -1, d)[:, :, :, rows]
+    return out, int(n.item()), x
+
+
+@pytest.mark.parametrize("lens,other", [
+    ([10, 30], [30, 10]), ([10, 0, 30], [10, 30, 0]), ([5, 5, 5], [5, 4, 6]),
+    ([3] * 400 + [7] * 624, [3] * 399 + [7, 3] + [7] * 623), ([40], None), ([0, 17], None)])
+def test_load_compares_the_length_of_every_request(lens, other):
+    """Requests of the stream cut elsewhere than the caller's: refused, nothing is stored."""
+    L, H, d, g = 1, 2, 128, 64
+    buf, n, x = paged_stream(lens, L, H, d, g, 11)
+    T = sum(lens)
+    pages = -(-T // 16) + 1
+    c = make(d, g, L, H, pages, 16)
+    at = torch.from_numpy(slots_for(T, pages, 16)).cuda()
+    if other is not None:
+        before = c.pool.clone()
+        with pytest.raises(kvc.KvcError) as e:
+            c.load(buf, n, at, other, check=True)
+        assert e.value.status == CORRUPT and torch.equal(c.pool, before)
+    c.load(buf, n, at, lens, check=True)
+    for i, y in enumerate(c.read(at)):
+        assert torch.equal(y.transpose(1, 2).view(torch.int16), x[:, i].view(torch.int16))

@@ -396,7 +396,8 @@ kvc_status kvc_attend(const void *in, size_t in_bytes, const kvc_attn_desc *attn
  * Status. These calls do not clear the status word that they are given
  * (DEVICE, 4 bytes, 4-byte aligned, may be null): one word collects the first
  * data-dependent error of a whole step's calls over many layers. Clear it
- * with kvc_cache_status_clear, read it with kvc_stream_status.
+ * with kvc_cache_status_clear, read it with kvc_stream_status. (kvc_cache_load
+ * has a word of its own, in its workspace; kvc_cache_load_noting both.)
  *
  * Concurrency. Calls that write the same slots, or share a workspace, must
  * not overlap (two captured graphs included). All pointers belong to the
@@ -481,6 +482,14 @@ size_t kvc_cache_load_workspace_bytes(const kvc_cache_desc *cache, const int32_t
 kvc_status kvc_cache_load(const void *in, size_t in_bytes, const kvc_cache_desc *cache,
                           const int32_t *seq_lens, int32_t n_requests, const int64_t *slots,
                           void *workspace, size_t workspace_bytes, kvc_stream_t stream);
+
+/* kvc_cache_load whose first data-dependent error is also noted in `status`, the word
+ * that the other calls share (not cleared here; may be null): for loads that
+ * nobody waits for, and captured ones. */
+kvc_status kvc_cache_load_noting(const void *in, size_t in_bytes, const kvc_cache_desc *cache,
+                                 const int32_t *seq_lens, int32_t n_requests,
+                                 const int64_t *slots, void *workspace, size_t workspace_bytes,
+                                 uint32_t *status, kvc_stream_t stream);
 
 /* The sign seed with which a stream of this description's layers alone has the
  * description's diagonals (pass it as kvc_params.sign_seed): sign_seed itself

@@ -34,7 +34,7 @@ EXPORTS = ["kvc_max_compressed_bytes", "kvc_workspace_bytes", "kvc_compress",
            "kvc_decompress_timed", "kvc_attend_workspace_bytes", "kvc_attend",
            "kvc_attend_timed", "kvc_cache_block_bytes", "kvc_cache_stream_seed",
            "kvc_cache_status_clear", "kvc_cache_write", "kvc_cache_read",
-           "kvc_cache_load_workspace_bytes", "kvc_cache_load",
+           "kvc_cache_load_workspace_bytes", "kvc_cache_load", "kvc_cache_load_noting",
            "kvc_cache_attend_workspace_bytes", "kvc_cache_attend", "kvc_test_e2m1", "kvc_test_div_const",
            "kvc_test_rcp_scale"]
 
@@ -177,6 +177,9 @@ def lib() -> C.CDLL:
                 ("kvc_cache_load", C.c_int, [C.c_void_p, C.c_size_t, K, C.POINTER(C.c_int32),
                                              C.c_int32, C.c_void_p, C.c_void_p, C.c_size_t,
                                              C.c_void_p]),
+                ("kvc_cache_load_noting", C.c_int, [C.c_void_p, C.c_size_t, K, C.POINTER(C.c_int32),
+                                                    C.c_int32, C.c_void_p, C.c_void_p, C.c_size_t,
+                                                    C.c_void_p, C.c_void_p]),
                 ("kvc_cache_attend_workspace_bytes", C.c_size_t, [K, T]),
                 ("kvc_cache_attend", C.c_int, [K, T, C.c_void_p, C.c_size_t, C.c_void_p,
                                                C.c_void_p])):
@@ -327,6 +330,13 @@ def kvc_cache_load(in_ptr, in_bytes, cache, seq_lens, slots_ptr, ws_ptr, ws_byte
     arr = (C.c_int32 * max(len(seq_lens), 1))(*seq_lens)
     return lib().kvc_cache_load(in_ptr, in_bytes, C.byref(cache), arr, len(seq_lens), slots_ptr,
                                 ws_ptr, ws_bytes, stream)
+
+
+def kvc_cache_load_noting(in_ptr, in_bytes, cache, seq_lens, slots_ptr, ws_ptr, ws_bytes, status_ptr,
+                          stream) -> int:
+    arr = (C.c_int32 * max(len(seq_lens), 1))(*seq_lens)
+    return lib().kvc_cache_load_noting(in_ptr, in_bytes, C.byref(cache), arr, len(seq_lens), slots_ptr,
+                                       ws_ptr, ws_bytes, status_ptr, stream)
 
 
 def kvc_cache_attend_workspace_bytes(cache, attn) -> int:
@@ -617,8 +627,8 @@ class PagedCache:
 
     def load(self, stream_buf, nbytes: int, slots, seq_lens, stream=None, check: bool = False):
         """Puts a compressed stream's codes into ``slots`` (one per token, requests in
-        order). Its own status word is read with check=True (which waits); else it
-        goes unread, and a bad stream shows only in ``load``'s workspace."""
+        order). An error in the stream or the slots goes to the status word that ``check``
+        reads; with check=True (which waits for the load) it raises here instead."""
         import torch
         if slots.dtype is not torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
             raise ValueError("slots: expects a contiguous int64 vector")
@@ -632,8 +642,9 @@ class PagedCache:
         seq, L, D = (C.c_int32 * (n or 1))(*map(int, seq_lens)), lib(), C.byref(self.desc)
         self._with_workspace(
             "kvc_cache_load", stream, s, lambda: L.kvc_cache_load_workspace_bytes(D, seq, n),
-            lambda at, size: L.kvc_cache_load(stream_buf.data_ptr(), int(nbytes), D, seq, n,
-                                              slots.data_ptr(), at, size, s),
+            lambda at, size: L.kvc_cache_load_noting(stream_buf.data_ptr(), int(nbytes), D, seq, n,
+                                                     slots.data_ptr(), at, size,
+                                                     None if check else self._status, s),
             (lambda at: kvc_stream_status(at, s)) if check else None)
 
     def attend(self, q, page_table, seq_lens, q_starts=None, max_q: int = 1, out=None, lse=None,

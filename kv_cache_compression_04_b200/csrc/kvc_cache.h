@@ -43,6 +43,7 @@ struct LoadArgs {
   uint32_t group;
   uint32_t table_fits;    // 1: in_bytes reach past the token table
   uint64_t tokens_at;     // of the token table, for the chunks that the caller's numbers give
+  uint32_t *note;         // the caller's status word, beside the workspace's; may be null
   const int64_t *slots;
   uint32_t lens[KVC_MAX_REQUESTS];
 };

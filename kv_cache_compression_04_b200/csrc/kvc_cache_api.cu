@@ -225,16 +225,17 @@ size_t kvc_cache_load_workspace_bytes(const kvc_cache_desc *cache, const int32_t
   return load_shape(cache, seq_lens, n_requests, s) == KVC_OK ? size_t(s.total) : 0;
 }
 
-kvc_status kvc_cache_load(const void *in, size_t in_bytes, const kvc_cache_desc *cache,
-                          const int32_t *seq_lens, int32_t n_requests, const int64_t *slots,
-                          void *workspace, size_t workspace_bytes, kvc_stream_t stream) {
+kvc_status kvc_cache_load_noting(const void *in, size_t in_bytes, const kvc_cache_desc *cache,
+                                 const int32_t *seq_lens, int32_t n_requests,
+                                 const int64_t *slots, void *workspace, size_t workspace_bytes,
+                                 uint32_t *status, kvc_stream_t stream) {
   LoadShape s;
   kvc_status st = load_shape(cache, seq_lens, n_requests, s);
   if (st != KVC_OK) return st;
   CachePool p;
   st = check_cache(cache, p);
   if (st != KVC_OK) return st;
-  if (!in || !aligned(in, 16) || !workspace || !aligned(workspace, 16) ||
+  if (!in || !aligned(in, 16) || !workspace || !aligned(workspace, 16) || !aligned(status, 4) ||
       (s.vectors > 0 && (!slots || !aligned(slots, 8))))
     return KVC_ERR_INVALID_ARG;
   if (workspace_bytes < s.total) return KVC_ERR_CAPACITY;
@@ -260,11 +261,19 @@ kvc_status kvc_cache_load(const void *in, size_t in_bytes, const kvc_cache_desc 
   a.table_fits = a.tokens_at + 4 * uint64_t(n_requests) <= in_bytes ? 1u : 0u;
   for (int32_t i = 0; i < n_requests; ++i) a.lens[i] = uint32_t(seq_lens[i]);
   a.slots = slots;
+  a.note = status;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(workspace, 0, kWsCtl, cs) != cudaSuccess) return KVC_ERR_CUDA;
   return launch_cache_load(cache->head_dim, cache->group_size, p, a, sms, cs) == cudaSuccess
              ? KVC_OK
              : KVC_ERR_CUDA;
+}
+
+kvc_status kvc_cache_load(const void *in, size_t in_bytes, const kvc_cache_desc *cache,
+                          const int32_t *seq_lens, int32_t n_requests, const int64_t *slots,
+                          void *workspace, size_t workspace_bytes, kvc_stream_t stream) {
+  return kvc_cache_load_noting(in, in_bytes, cache, seq_lens, n_requests, slots, workspace,
+                               workspace_bytes, nullptr, stream);
 }
 
 size_t kvc_cache_attend_workspace_bytes(const kvc_cache_desc *cache, const kvc_cache_attn *attn) {

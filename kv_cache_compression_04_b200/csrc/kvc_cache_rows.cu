@@ -329,6 +329,10 @@ __global__ void __launch_bounds__(kRowThreads)
 // entry that a vector relies on is checked by the lanes that use it: its code
 // chunk raw and in place, its meta chunk raw inside the stream or eliminated
 // (then expanded, and checked, by meta_expand_kernel).
+__device__ __forceinline__ void load_error(const LoadArgs &a, uint32_t code) {
+  set_status(a.d.status, code);
+  note(a.note, code);
+}
 template <int D, int G>
 __global__ void __launch_bounds__(kRowThreads)
     cache_load_kernel(const __grid_constant__ CachePool c, const __grid_constant__ LoadArgs a) {
@@ -340,6 +344,8 @@ __global__ void __launch_bounds__(kRowThreads)
   // same time, where the table is if the header is right.
   bool bad = false;
   if (threadIdx.x == 0) {
+    if (blockIdx.x == 0)
+      if (const uint32_t e = *a.d.status) note(a.note, e);  // of the meta expansion
     const StreamHdr h = parse_header<D>(a.d);
     bool ok = h.ok && h.bits == 4 && h.group == a.group && h.quant <= 1 && !h.code_elim &&
               h.vec_signs == c.vec_signs && h.seed == c.seed &&
@@ -351,7 +357,7 @@ __global__ void __launch_bounds__(kRowThreads)
       bad |= ld_u32(in + a.tokens_at + 4 * r) != a.lens[r];
   }
   if (__syncthreads_or(bad)) {
-    if (threadIdx.x == 0) set_status(a.d.status, KVC_ERR_CORRUPT);
+    if (threadIdx.x == 0) load_error(a, KVC_ERR_CORRUPT);
     return;
   }
   const uint64_t base = base_s, code_bytes = uint64_t(a.d.V) * C::CB;
@@ -368,7 +374,7 @@ __global__ void __launch_bounds__(kRowThreads)
     const int64_t s64 = __ldg(reinterpret_cast<const long long *>(a.slots) + t);
     if (s64 < 0) continue;
     if (s64 >= int64_t(c.slots)) {
-      set_status(a.d.status, KVC_ERR_CORRUPT);
+      load_error(a, KVC_ERR_CORRUPT);
       continue;
     }
     const uint32_t lk = lkh / c.heads, h = lkh - lk * c.heads, l = lk >> 1, kv = lk & 1;
@@ -381,7 +387,7 @@ __global__ void __launch_bounds__(kRowThreads)
     if (entry_size(e) != (rest < kChunk ? rest : uint64_t(kChunk)) || entry_pipe(e) != 0 ||
         entry_offset(e) != ck * kChunk ||
         (raw && (entry_pipe(em) != 0 || base + entry_offset(em) + mlen > stream_bytes))) {
-      set_status(a.d.status, KVC_ERR_CORRUPT);
+      load_error(a, KVC_ERR_CORRUPT);
       continue;
     }
     const uint32_t *src = reinterpret_cast<const uint32_t *>(in + base + uint64_t(v) * C::CB);

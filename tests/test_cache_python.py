@@ -60,3 +60,18 @@ def test_load_refuses_a_size_that_the_buffer_does_not_have(nbytes):
     """A negative one would reach the library as a size near 2^64."""
     with pytest.raises(ValueError):
         load(HostCache(), [5], nbytes)
+
+
+def test_load_noting_checks_its_status_word():
+    """kvc_cache_load's checks, and the status word's alignment."""
+    fake, c, seq = 0x7F0000000000, HostCache().desc, [5, 0, 9]
+    c.pool = fake
+    size = kvc.kvc_cache_load_workspace_bytes(c, seq)
+
+    def call(status, ws=size, lens=seq):
+        return kvc.kvc_cache_load_noting(fake, 4096, c, lens, fake, fake, ws, status, None)
+
+    assert call(fake + 4) == call(None) == ENQUEUED
+    assert call(fake + 2) == kvc.KVC_ERR_INVALID_ARG
+    assert call(fake, size - 1) == kvc.KVC_ERR_CAPACITY
+    assert call(fake, size, [5, -1]) == kvc.KVC_ERR_INVALID_ARG

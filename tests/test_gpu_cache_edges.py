@@ -55,3 +55,56 @@ def test_load_compares_the_length_of_every_request(lens, other):
     c.load(buf, n, at, lens, check=True)
     for i, y in enumerate(c.read(at)):
         assert torch.equal(y.transpose(1, 2).view(torch.int16), x[:, i].view(torch.int16))
+
+
+def test_a_load_that_nobody_waits_for_leaves_its_error():
+    """Of the header, of a slot, of an eliminated meta chunk: in the cache's status word;
+    with check=True in the exception alone."""
+    d, g, L, H, T, seed = 128, 32, 1, 2, 3000, 5
+    kv = narrow_meta(L, H, T, d, g, seed, 1)
+    buf, n, _ = stream_of(kv, g, seed, 0, 0, 1)
+    pages = T // 16 + 2
+    c = make(d, g, L, H, pages, 16, 0, 1, seed)
+    at = torch.from_numpy(slots_for(T, pages, 16)).cuda()
+    c.load(buf, n, at, [T])
+    assert status_of(c) == kvc.KVC_OK
+    c.load(buf, n - 1, at, [T])  # cut short
+    assert status_of(c) == CORRUPT and status_of(c) == kvc.KVC_OK
+    far = at.clone()
+    far[77] = pages * 16
+    c.load(buf, n, far, [T])
+    assert status_of(c) == CORRUPT
+    n_code = -(-L * 2 * H * T * d // 2 // 16384)
+    odd = buf.clone()
+    entry = odd[64 + 8 * n_code: 72 + 8 * n_code]
+    assert int(entry[0]) + 256 * int(entry[1]) < 16384  # the first meta chunk is eliminated
+    entry[0], entry[1] = 8, 0                           # shorter than its bitmap
+    c.load(odd, n, at, [T])
+    assert status_of(c) == CORRUPT
+    for bad, slots in ((odd, at), (buf, far)):
+        with pytest.raises(kvc.KvcError):
+            c.load(bad, n, slots, [T], check=True)
+        assert status_of(c) == kvc.KVC_OK
+
+
+def test_a_captured_load_leaves_its_error():
+    d, g, L, H, T = 64, 64, 2, 2, 50
+    kv = torch.randn(L, 2, H, T, d, device="cuda").to(torch.bfloat16)
+    buf, n, back = stream_of(kv, g, 11, 0, 0, 0)
+    c = make(d, g, L, H, 6, 16)
+    at = torch.from_numpy(slots_for(T, 6, 16)).cuda()
+    c.load(buf, n, at, [T])  # (its kernels are known to the device)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.load(buf, n, at, [T])
+    c.pool.zero_()
+    graph.replay()
+    c.check()
+    k, v = c.read(at)
+    assert torch.equal(k.transpose(1, 2), back[:, 0]) and torch.equal(v.transpose(1, 2), back[:, 1])
+    buf[40] ^= 1  # another sign seed
+    graph.replay()
+    assert status_of(c) == CORRUPT
+    buf[40] ^= 1
+    graph.replay()
+    assert status_of(c) == kvc.KVC_OK

@@ -496,8 +496,10 @@ __device__ __forceinline__ void pf_unpack(const CacheAttnArgs &a, uint8_t *smem,
         }
         const uint32_t ex = (__float_as_uint(bound) >> 23) & 255u;
         const bool none = bad || bound == 0.f;
-        const float scale = none ? 1.f : __uint_as_float(ex << 23);
-        const float inv = none ? (bad ? 0.f : 1.f) : __uint_as_float((254u - ex) << 23);
+        // (zeros weigh nothing: with a scale of 1 their weights, scaled up for small values
+        // beside them, passed fp16's range)
+        const float scale = none ? 0.f : __uint_as_float(ex << 23);
+        const float inv = none ? 0.f : __uint_as_float((254u - ex) << 23);
         float sv[NG], zv[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -553,7 +555,7 @@ __device__ __forceinline__ void pf_unpack(const CacheAttnArgs &a, uint8_t *smem,
           meta[(2 * NG + 1) * NK + row] = bias;
         }
         odd |= !w.in[x] || bad;
-        most = max(most, none ? 0u : __float_as_uint(scale));
+        most = max(most, __float_as_uint(scale));
       }
       most = __reduce_max_sync(0xFFFFFFFFu, most);
       odd = __any_sync(0xFFFFFFFFu, odd);

@@ -108,3 +108,27 @@ def test_a_captured_load_leaves_its_error():
     buf[40] ^= 1
     graph.replay()
     assert status_of(c) == kvc.KVC_OK
+
+
+# ----------------------------------------------------------- attention --
+@pytest.mark.parametrize("d,g", KINDS)
+@pytest.mark.parametrize("asked", [1, 2, 9, 60])
+@pytest.mark.parametrize("size", [2.0 ** -12, 2.0 ** -17])
+def test_zero_values_among_small_ones(d, g, asked, size):
+    """Rows of zeros (padding that a model left in) beside values of 1e-4 and less."""
+    n, qpk = 200, 4
+    c = make(d, g, 1, 1, 14, 16)
+    k, v = rows(1, n, 1, d)
+    v = v * size
+    v[:, ::3] = 0
+    c.write(k, v, torch.arange(n, device="cuda"))
+    q = torch.randn(1, asked, qpk, d, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    out = c.attend(q.cuda(), torch.arange(13, dtype=torch.int32, device="cuda")[None], dev([n]),
+                   q_starts=dev([0, asked]), max_q=asked) / size
+    c.check()
+    x, spread = cache_values(c, np.arange(n))
+    o, _, mag, s = ref.attend(x, q.double().numpy(), qpk, d ** -0.5,
+                              [(0, n - asked + i + 1) for i in range(asked)], spread)
+    tol = 2.0 ** -8 * np.abs(o) + (2 * (2.0 ** -18 * s + 2.0 ** -20) + 2.0 ** -11)[..., None] * mag * 1.01
+    bad = np.abs(out.double().cpu().numpy() - o / size) - tol / size
+    assert (bad <= 1e-7).all(), bad.max()

@@ -21,15 +21,20 @@ __device__ __forceinline__ float half_hi(uint32_t m) {
   return __half2float(__ushort_as_half(uint16_t(m >> 16)));
 }
 
-// n - 8 of the codes in bits 0..3 (kHigh: 4..7) of both halves, as fp16 pairs.
-template <bool kHigh>
-__device__ __forceinline__ uint32_t centred(uint32_t x) {
+// n - kFrom of the codes n in bits 0..3 (kHigh: 4..7) of both halves, as fp16 pairs.
+template <bool kHigh, int kFrom>
+__device__ __forceinline__ uint32_t codes_less(uint32_t x) {
+  constexpr uint32_t one = kHigh ? 0x5400u + 16 * kFrom : 0x6400u + kFrom;  // 64 (1024) + kFrom
   uint32_t t, d;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
       : "=r"(t)
       : "r"(x), "n"(kHigh ? 0x00F000F0 : 0x000F000F), "n"(kHigh ? 0x54005400 : 0x64006400));
-  asm("sub.f16x2 %0, %1, %2;" : "=r"(d) : "r"(t), "r"(kHigh ? 0x54805480u : 0x64086408u));
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(d) : "r"(t), "r"(one << 16 | one));
   return d;
+}
+template <bool kHigh>
+__device__ __forceinline__ uint32_t centred(uint32_t x) {
+  return codes_less<kHigh, 8>(x);
 }
 // Whether a meta word's scale or zero is infinite or NaN.
 __device__ __forceinline__ bool not_finite(uint32_t m) {

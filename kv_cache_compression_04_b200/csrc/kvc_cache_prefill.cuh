@@ -10,7 +10,10 @@
 //         exact where keys rounded to fp16 would not be;
 //   P     = softmax weights in fp16, written to tensor memory (over the scores) as the
 //         next product's operand;
-//   O    += P V, V dequantised to fp16 (rounded once, as P is): 128 x D.
+//   O    += P V, V dequantised to fp16 (rounded once, as P is): 128 x D. V = z + n s times
+//         a power of two per key: z and s stay exact there, so one fused multiply-add
+//         rounds. (With z + 8 s and n - 8 the sum was rounded before it: the same for all
+//         channels of a group, which the inverse transform puts into one.)
 // Floor per 128 x 64 tile pair at d = 128: 3 x 256 cycles of the tensor cores (hi and
 // lo parts, values). Measured: 1024 queries x 32 heads over 9216 keys in 255 us (574
 // TFLOP/s of the two products counted once), about 1750 cycles a tile, of which the
@@ -439,7 +442,7 @@ __device__ __forceinline__ void pf_unpack(const CacheAttnArgs &a, uint8_t *smem,
         w.in[x] = pg[x] >= 0 && uint32_t(pg[x]) < a.c.num_pages;
         if (pg[x] != -1 && !w.in[x] && a.status) set_status(a.status, KVC_ERR_CORRUPT);
 #pragma unroll
-        for (int q = 0; q < W; ++q) w.k[x][q] = w.v[x][q] = 0x88888888u;  // n - 8 = 0
+        for (int q = 0; q < W; ++q) w.k[x][q] = w.v[x][q] = 0x88888888u;  // (n - 8 = 0; meta 0)
 #pragma unroll
         for (int g = 0; g < NG; ++g) w.mk[x][g] = w.mv[x][g] = 0;
         if (w.in[x]) {
@@ -503,9 +506,9 @@ __device__ __forceinline__ void pf_unpack(const CacheAttnArgs &a, uint8_t *smem,
         float sv[NG], zv[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const uint32_t m = bad ? 0u : w.mv[x][g];
+          const uint32_t m = bad ? 0u : w.mv[x][g];  // (|z|, 15 |s| <= 2 bound)
           sv[g] = half_lo(m) * inv;
-          zv[g] = zero8(m) * inv;
+          zv[g] = half_hi(m) * inv;
         }
         // a lane's words in an order of its own (q ^ flip): in step, eight lanes' pieces
         // would meet in two columns of the banks (17 of 43 million wavefronts)
@@ -539,8 +542,8 @@ __device__ __forceinline__ void pf_unpack(const CacheAttnArgs &a, uint8_t *smem,
             return d;
           };
           *reinterpret_cast<uint4 *>(vr + (wj >> 3) * NK * 128 + (((wj & 7) ^ sw) << 4)) =
-              make_uint4(deq(centred<false>(u)), deq(centred<true>(u)), deq(centred<false>(u >> 8)),
-                         deq(centred<true>(u >> 8)));
+              make_uint4(deq(codes_less<false, 0>(u)), deq(codes_less<true, 0>(u)),
+                         deq(codes_less<false, 0>(u >> 8)), deq(codes_less<true, 0>(u >> 8)));
         }
         if (int(p) < NG) {
           uint32_t m = w.mk[x][0];

@@ -132,3 +132,41 @@ def test_zero_values_among_small_ones(d, g, asked, size):
     tol = 2.0 ** -8 * np.abs(o) + (2 * (2.0 ** -18 * s + 2.0 ** -20) + 2.0 ** -11)[..., None] * mag * 1.01
     bad = np.abs(out.double().cpu().numpy() - o / size) - tol / size
     assert (bad <= 1e-7).all(), bad.max()
+
+
+@pytest.mark.parametrize("d,g", KINDS)
+def test_values_of_blocks_of_128_are_rounded_once(d, g):
+    """One key per request, seen by 80 rows: out is that value, its transformed channels
+    rounded to fp16 once (times a power of two), the inverse transform in fp32 and one more
+    rounding. Channels far from zero whose steps are fractions of an fp16 step show a rounding
+    of z + 8 s of its own."""
+    R, asked, qpk, page = 24, 20, 4, 16
+    c = make(d, g, 1, 1, R, page, signs=1, fill=0)
+    rng = np.random.default_rng(d + g)
+    at = np.arange(R) * page
+    # codes at random; zeros of 1 .. 2 and scales of odd multiples of 2^-14: z + 8 s lies
+    # halfway between fp16 values
+    host = c.pool.cpu().numpy()
+    cb, mb = d // 2, d // g * 4
+    t = host.reshape(R, 2, 16 * (cb + mb))
+    t[:, :, :cb] = rng.integers(0, 256, (R, 2, cb))
+    meta = np.zeros((R, 2, d // g, 2), np.float16)
+    meta[..., 0] = (2 * rng.integers(0, 8, meta.shape[:-1]) + 1) * 2.0 ** -14
+    meta[..., 1] = 1 + rng.integers(0, 500, meta.shape[:-1]) * 2.0 ** -10
+    t[:, :, 16 * cb:16 * cb + mb] = meta.view(np.uint8).reshape(R, 2, mb)
+    c.pool.copy_(torch.from_numpy(host))
+    q = torch.randn(1, R * asked, qpk, d, device="cuda").half()
+    out = c.attend(q, torch.arange(R, dtype=torch.int32, device="cuda")[:, None], dev([1] * R),
+                   q_starts=dev([asked * i for i in range(R + 1)]), max_q=asked, causal=False)
+    c.check()
+    codes, m = ref.rows_of(c.pool.cpu().numpy(), at, d, g, page)
+    y = ref.grid_values(codes, m, g)[0, 1, 0]  # [R, d]; its fp16 grid: 2^-10 of the power of two below 8 z
+    y16 = (y / 8).astype(np.float16).astype(np.float64) * 8
+    assert np.abs(y16 - y).max() > 2.0 ** -9
+    sg = ref.signs(11, 1, 1, 1, d)[0, 1, 0]
+    want = (y16 @ ref.hadamard(d) / d * sg).repeat(asked * qpk, 0).reshape(R * asked, qpk, d)
+    # half a step of the output; the weight's exponent (2^-21 of it); fp32: the merge's weights,
+    # 1 / (L d) and seven sums, of sum |y| / d
+    tol = (2.0 ** -11 + 2.0 ** -21) * np.abs(want) + 2.0 ** -25 + 10 * 2.0 ** -24 * np.abs(y).mean(-1).max()
+    bad = np.abs(out[0].double().cpu().numpy() - want) - tol
+    assert (bad <= 0).all(), bad.max()

@@ -371,8 +371,8 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
       if ((asked & 15u) == 0) {
         off_l = -1;
         const uint32_t i = asked + (lane >> 1), tile = 2 * (s.first + i) + (lane & 1);
-        const int32_t t0 = int32_t(tile * kTileTok);
-        if (i < mine && tile <= last && t0 < s.any_hi && t0 + kTileTok > s.any_lo) {
+        const int32_t t0 = int32_t(tile * kTileTok);  // (t0 + 16 may be 2^31)
+        if (i < mine && tile <= last && t0 < s.any_hi && t0 > s.any_lo - kTileTok) {
           const uint32_t pi = fdiv(a.tpp, tile);
           const int32_t pg = __ldg(table + pi);
           if (pg >= 0 && uint32_t(pg) < a.c.num_pages)
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
           load_words<NG>(vt + x * C::TB + 16 * C::CB + tB * 4 * NG, vB[x]);
         }
         // no key is hidden from any row
-        const bool all = got == 3 && t0 >= s.all_lo && t0 + kChunkTok <= s.all_hi;
+        const bool all = got == 3 && t0 >= s.all_lo && t0 <= s.all_hi - kChunkTok;
         if (!all) {
           int2 lim[R];
 #pragma unroll

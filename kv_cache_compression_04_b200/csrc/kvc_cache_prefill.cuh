@@ -851,7 +851,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           }
         }
         const uint4 odd = *reinterpret_cast<const uint4 *>(smem + C::wodd + buf * 16);
-        if ((odd.x | odd.y | odd.z | odd.w) || t0 < s.all_lo || t0 + NK > s.all_hi) {
+        if ((odd.x | odd.y | odd.z | odd.w) || t0 < s.all_lo || t0 > s.all_hi - NK) {
 #pragma unroll
           for (int x = 0; x < NK; ++x) {
             const int32_t t = t0 + x;

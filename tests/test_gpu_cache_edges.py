@@ -170,3 +170,22 @@ def test_values_of_blocks_of_128_are_rounded_once(d, g):
     tol = (2.0 ** -11 + 2.0 ** -21) * np.abs(want) + 2.0 ** -25 + 10 * 2.0 ** -24 * np.abs(y).mean(-1).max()
     bad = np.abs(out[0].double().cpu().numpy() - want) - tol
     assert (bad <= 0).all(), bad.max()
+
+
+@pytest.mark.parametrize("qpk,asked", [(4, 1), (8, 1), (8, 3), (16, 3), (4, 30)])
+@pytest.mark.parametrize("n", [2 ** 31 - 1, 2 ** 31 - 14, 2 ** 31 - 16, 2 ** 31 - 40])
+def test_the_longest_requests(qpk, asked, n):
+    """Lengths up to 2^31 - 1, of which a window shows the last tokens: a page that stands in
+    every entry of the table."""
+    d, g, page, window = 64, 64, 65536, 45
+    c = make(d, g, 1, 1, 1, page, fill=0)
+    m = 300  # the page's last slots
+    at = torch.arange(page - m, page, device="cuda")
+    c.write(*rows(1, m, 1, d), at)
+    q = torch.randn(1, asked, qpk, d, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    tab = torch.zeros(1, 2 ** 31 // page, dtype=torch.int32, device="cuda")
+    out = c.attend(q.cuda(), tab, dev([n]), q_starts=dev([0, asked]), max_q=asked, window=window)
+    c.check()
+    end = m - (2 ** 31 - n)  # the length, counted from the first of those slots
+    lim = [(end - asked + i + 1 - window, end - asked + i + 1) for i in range(asked)]
+    close(c, at.cpu().numpy(), q, out, qpk, lim, d ** -0.5, torch.bfloat16)

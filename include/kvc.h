@@ -528,7 +528,8 @@ typedef struct {
   int32_t window;             /* 0: none */
   float scale;
   int32_t reserved;           /* 0 */
-  int64_t q_tokens;           /* rows of q, 0 .. 2^24 */
+  int64_t q_tokens;           /* rows of q, 0 .. 2^24; layers * q_tokens * query heads
+                                 below 2^31 */
   const int32_t *q_starts;    /* DEVICE [n_requests + 1], or null */
   const int32_t *seq_lens;    /* DEVICE [n_requests] */
   const int32_t *page_table;  /* DEVICE [n_requests][page_table_pages] */

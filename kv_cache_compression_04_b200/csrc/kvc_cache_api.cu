@@ -158,6 +158,8 @@ kvc_status check_attn(const kvc_cache_desc *cache, const kvc_cache_attn *t, Cach
   // (query rows of a request, and units, are counted in 32 bits; a CTA has 32 of 128 rows)
   if (units * (cols > 16 ? 4 : 1) >= (uint64_t(1) << 31) - 1 || uint64_t(t->q_tokens) * qpk >= (uint64_t(1) << 31))
     return KVC_ERR_UNSUPPORTED;
+  // (the merge has a CTA per row at most)
+  if (lh * qpk * uint64_t(t->q_tokens) >= (uint64_t(1) << 31)) return KVC_ERR_UNSUPPORTED;
   w.shapes = round256(8 * ((cols > 16 ? w.blocks : reqs) + 1));
   w.frags = w.shapes + round256(16 * reqs);
   w.queries = w.frags + (cols > 16 ? round256(16 * w.blocks) : 0);

@@ -218,8 +218,7 @@ template <int D, class At>
 cudaError_t launch_combine(int dtype, bool wide, const CacheAttnArgs &a, uint32_t grid,
                            cudaStream_t st) {
   const uint64_t rows = uint64_t(a.c.layers) * a.q_tokens * a.c.heads * a.qpk;
-  const uint64_t cg = wide ? rows : (rows + 3) / 4;
-  if (cg >= (uint64_t(1) << 31)) return cudaErrorInvalidValue;
+  const uint64_t cg = wide ? rows : (rows + 3) / 4;  // (below 2^31: checked before the first kernel)
   auto ck = dtype == KVC_BF16 ? (wide ? cache_combine_kernel<D, At, KVC_BF16, 8>
                                       : cache_combine_kernel<D, At, KVC_BF16, 1>)
                               : (wide ? cache_combine_kernel<D, At, KVC_FP16, 8>

@@ -75,3 +75,14 @@ def test_load_noting_checks_its_status_word():
     assert call(fake + 2) == kvc.KVC_ERR_INVALID_ARG
     assert call(fake, size - 1) == kvc.KVC_ERR_CAPACITY
     assert call(fake, size, [5, -1]) == kvc.KVC_ERR_INVALID_ARG
+
+
+def test_attention_of_too_many_rows_is_refused():
+    """2^31 rows of out in all: refused with the arguments, not after two kernels."""
+    fake, c = 0x7F0000000000, kvc.kvc_cache_desc(64, 8, 128, 4, 128, 0, 0, 0, 0, 16, 0, 4, 0x7F0000000000)
+    for tokens, starts, max_q in ((1 << 20, fake, 1), (1 << 20, fake, 500)):
+        for n, want in ((tokens - 1, ENQUEUED), (tokens, kvc.KVC_ERR_UNSUPPORTED)):
+            t = kvc.kvc_cache_attn(0, 4, 3, max_q, 1, 0, 0.1, 0, n, starts, fake, fake, 10, 10, fake,
+                                   n * 4096, 4096, 128, fake, n * 4096, 4096, 128, None)
+            assert (kvc.kvc_cache_attend_workspace_bytes(c, t) == 0) == (n == tokens)
+            assert kvc.kvc_cache_attend(c, t, fake, 1 << 60, None, None) == want

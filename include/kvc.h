@@ -510,7 +510,8 @@ uint64_t kvc_cache_stream_seed(const kvc_cache_desc *cache);
  * sums are held in fp32, out is rounded once to dtype. A query that sees no key
  * gives zeros and lse -inf. Rows of q that no request names are left as they
  * were in out and lse; NaN and infinities in slots past a request's length are
- * never used. A request whose q_starts or seq_lens is out of range (decreasing
+ * never used; a visible value stored as NaN makes out NaN and leaves lse as it
+ * is. A request whose q_starts or seq_lens is out of range (decreasing
  * or outside [0, q_tokens]; more than max_q queries; a length below 0 or past
  * its row of the page table) sets KVC_ERR_CORRUPT and its rows are left as they
  * were (where q_starts decrease, the other requests' rows are unspecified); a

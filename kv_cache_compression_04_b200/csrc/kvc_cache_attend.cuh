@@ -544,8 +544,9 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
               if (!there || b0 < lim[i].x || b0 >= lim[i].y) sc[x][i][1] = -INFINITY;
             }
             // A value whose scale or zero is not finite: the rows that see the key get
-            // NaN through its score, the others (and slots that no row sees, which may
-            // hold anything) weigh it 0.
+            // NaN through their sums of zeros (one group's are enough: the inverse transform
+            // mixes all channels), the others (and slots that no row sees, which may
+            // hold anything) weigh it 0. Scores and the log-sum-exp do not depend on values.
             bool odd_a = false, odd_b = false;
 #pragma unroll
             for (int gg = 0; gg < NG; ++gg) {
@@ -554,8 +555,8 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
             }
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-              if (odd_a && sc[x][i][0] != -INFINITY) sc[x][i][0] = __uint_as_float(0x7FFFFFFFu);
-              if (odd_b && sc[x][i][1] != -INFINITY) sc[x][i][1] = __uint_as_float(0x7FFFFFFFu);
+              const bool sees = (odd_a && sc[x][i][0] != -INFINITY) || (odd_b && sc[x][i][1] != -INFINITY);
+              if (sees) z[i][0] = __uint_as_float(0x7FFFFFFFu);
             }
             // (slots that no row sees must not widen the range of scales either)
             const bool no_a = odd_a || a0 < s.any_lo || a0 >= s.any_hi;

@@ -64,7 +64,8 @@ struct PfCfg {
   static constexpr size_t v = k + kPfStages * KBUF;
   static constexpr size_t meta = v + kPfStages * KBUF;
   static constexpr size_t fin = meta + kPfStages * size_t(MW) * NK * 4;  // [softmax][row] maximum, sum
-  static constexpr size_t wmax = fin + 2 * kPfRows * 8;         // [stage][unpacking warp]
+  static constexpr size_t taint = fin + 2 * kPfRows * 8;        // [softmax][row]
+  static constexpr size_t wmax = taint + 2 * kPfRows * 4;       // [stage][unpacking warp]
   static constexpr size_t wodd = wmax + kPfStages * 4 * 4;
   // full and values (a stage), scores and weights (a tile's scores), queries copied, ready
   static constexpr size_t bars = wodd + kPfStages * 4 * 4;
@@ -477,7 +478,7 @@ __device__ __forceinline__ void pf_unpack(const CacheAttnArgs &a, uint8_t *smem,
       uint8_t *kb = smem + C::k + buf * C::KBUF, *vb = smem + C::v + buf * C::KBUF;
       float *meta = reinterpret_cast<float *>(smem + C::meta) + buf * C::MW * NK;
       uint32_t most = 0;
-      bool odd = false;
+      uint32_t odd = 0;  // bit 0: a key that is not there, bit 1: a value that is not finite
 #pragma unroll
       for (int x = 0; x < RX; ++x) {
         const uint32_t row = r0 + 32 * x, sw = row & 7;
@@ -501,7 +502,7 @@ __device__ __forceinline__ void pf_unpack(const CacheAttnArgs &a, uint8_t *smem,
         const bool none = bad || bound == 0.f;
         // (zeros weigh nothing: with a scale of 1 their weights, scaled up for small values
         // beside them, passed fp16's range)
-        const float scale = none ? 0.f : __uint_as_float(ex << 23);
+        const float scale = none ? 0.f : __uint_as_float(ex << 23);  // (-0: not finite)
         const float inv = none ? 0.f : __uint_as_float((254u - ex) << 23);
         float sv[NG], zv[NG];
 #pragma unroll
@@ -552,16 +553,16 @@ __device__ __forceinline__ void pf_unpack(const CacheAttnArgs &a, uint8_t *smem,
           meta[p * NK + row] = half_lo(m);
           meta[(NG + p) * NK + row] = zero8(m);
         }
-        const float bias = !w.in[x] ? -INFINITY : bad ? __uint_as_float(0x7FFFFFFFu) : 0.f;
+        const float bias = !w.in[x] ? -INFINITY : 0.f;
         if (p == 3) {
-          meta[2 * NG * NK + row] = scale;
+          meta[2 * NG * NK + row] = bad ? -0.f : scale;
           meta[(2 * NG + 1) * NK + row] = bias;
         }
-        odd |= !w.in[x] || bad;
+        odd |= (w.in[x] ? 0u : 1u) | (bad ? 2u : 0u);
         most = max(most, __float_as_uint(scale));
       }
       most = __reduce_max_sync(0xFFFFFFFFu, most);
-      odd = __any_sync(0xFFFFFFFFu, odd);
+      odd = __reduce_or_sync(0xFFFFFFFFu, odd);
       if (lane == 0) {
         reinterpret_cast<uint32_t *>(smem + C::wmax)[buf * 4 + warp] = most;
         reinterpret_cast<uint32_t *>(smem + C::wodd)[buf * 4 + warp] = odd;
@@ -814,6 +815,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // Running state as in kvc_cache_attend.cuh: nm = -m (base 2, and - log2 of the
       // values' common exponent: weights times 2^(a value's e) reach up to 2^15).
       float nm = 0.f, mt = 0.f, thr = -INFINITY, l = 0.f, lw = 0.f, v_most = 0.f;
+      float *taint = reinterpret_cast<float *>(smem + C::taint) + which * kPfRows + row;
+      *taint = 0.f;  // NaN once the row has seen a value that is not finite
 
       for (uint32_t i = (which ^ j0) & 1u; i < s.tiles; i += 2) {
         const uint32_t j = j0 + i, buf = j % kPfStages, sb = j % C::NS, tS = tl + C::tS + sb * C::SW;
@@ -851,7 +854,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           }
         }
         const uint4 odd = *reinterpret_cast<const uint4 *>(smem + C::wodd + buf * 16);
-        if ((odd.x | odd.y | odd.z | odd.w) || t0 < s.all_lo || t0 > s.all_hi - NK) {
+        const uint32_t odds = odd.x | odd.y | odd.z | odd.w;
+        if (odds & 2u) {  // values that are not finite: out is NaN for the rows that see them
+#pragma unroll 1
+          for (int x = max(lo - t0, 0); x < min(hi - t0, NK); ++x)
+            if (__float_as_uint(meta[2 * NG * NK + x]) == 0x80000000u) *taint = __uint_as_float(0x7FFFFFFFu);
+        }
+        if ((odds & 1u) || t0 < s.all_lo || t0 > s.all_hi - NK) {
 #pragma unroll
           for (int x = 0; x < NK; ++x) {
             const int32_t t = t0 + x;
@@ -948,6 +957,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
       float *rec = a.rec + (s.unit + blockIdx.x) * uint64_t(kPfRows * (4 + D)) + row * (4 + D);
       const bool live = uint32_t(row) < s.nc;
+      const float bad = *taint;  // (in some columns is enough: the inverse transform mixes all)
       if (live && which == 0)
         *reinterpret_cast<float2 *>(rec) = make_float2(m, mine[0].y * w[0] + mine[1].y * w[1]);
 #pragma unroll
@@ -960,7 +970,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         tm_loaded16(o1);
 #pragma unroll
         for (int y = 0; y < 16; ++y)
-          o[y] = 8.f * ((has[0] ? o[y] * w[0] : 0.f) + (has[1] ? o1[y] * w[1] : 0.f));
+          o[y] = 8.f * ((has[0] ? o[y] * w[0] : 0.f) + (has[1] ? o1[y] * w[1] : 0.f)) + bad;
 #pragma unroll
         for (int y = 0; y < 16; y += 8) {
           // columns of stored word wj: halves of its two 32-channel blocks

@@ -189,3 +189,29 @@ def test_the_longest_requests(qpk, asked, n):
     end = m - (2 ** 31 - n)  # the length, counted from the first of those slots
     lim = [(end - asked + i + 1 - window, end - asked + i + 1) for i in range(asked)]
     close(c, at.cpu().numpy(), q, out, qpk, lim, d ** -0.5, torch.bfloat16)
+
+
+@pytest.mark.parametrize("d,g", [(128, 128), (128, 32), (64, 64)])
+@pytest.mark.parametrize("asked", [1, 2, 6, 12, 60])     # 4 .. 240 rows: every form
+@pytest.mark.parametrize("at", [3, 90, 95])  # in tiles that all queries see in full, and in the last one
+def test_lse_does_not_depend_on_values(d, g, asked, at):
+    """A value stored as NaN makes out NaN for the queries that see it and changes no lse."""
+    H, qpk, n = 1, 4, 97
+    c = make(d, g, 1, H, 8, 16)
+    kv = rows(1, n, H, d)
+    c.write(*kv, torch.arange(n, device="cuda"))
+    q = torch.randn(1, asked, qpk, d, device="cuda").to(torch.bfloat16)
+    tab, st = dev([list(range(7))]), dev([0, asked])
+    lse, want = (torch.empty(1, asked, qpk, device="cuda") for _ in range(2))
+    fine = c.attend(q, tab, dev([n]), q_starts=st, max_q=asked, lse=want)
+    c.check()
+    kv[1][0, at, 0, 5] = float("nan")
+    c.write(*kv, torch.arange(n, device="cuda"))
+    assert status_of(c) == kvc.KVC_ERR_NONFINITE
+    out = c.attend(q, tab, dev([n]), q_starts=st, max_q=asked, lse=lse)
+    c.check()
+    see = torch.tensor([n - asked + i >= at for i in range(asked)])
+    assert torch.isnan(out[0, see]).all()
+    # (the weights' common power of two may differ: one rounding of a sum of a few units, and exp2's)
+    assert (lse - want).abs().max() <= 2.0 ** -18
+    assert torch.isfinite(out[0, ~see]).all() and torch.isfinite(fine).all()

@@ -414,17 +414,27 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
     }
 
     // ---- running state of this lane's rows: LR per block, row (NB == 1 ? tq : 8 b +
-    // 2 tq + i). Scores are kept raw; m, in base 2, follows only jumps of more than
-    // 2^8 (weights reach 2^8; sums in fp32 lose nothing by it).
+    // 2 tq + i). Scores are kept raw; their maximum m, in base 2, follows only jumps of
+    // more than 2^8 (weights p = 2^(score - m) reach 2^8; sums in fp32 lose nothing by it).
+    // All sums hold p 2^lw, whose products with the values' scales s are the value product's
+    // weights: fp16, so lw keeps them in its range. Of two choices a row takes the larger,
+    //   5 - floor(log2 of the largest s so far): p s 2^lw < 2^14 for any p, and
+    //   -3 - log2 of the largest p s: where the largest s has little weight. (Without it one
+    //   visible value of 2^20 times the others' scale and no weight pushed their weights into
+    //   the subnormals: errors of 1.6e-3, at 2^24 of 0.11.)
+    // The largest p s is looked for where lw is chosen anew, when m rises or a scale comes
+    // that p 2^8 could take past 2^15; between, lw stands, and it never comes down further
+    // than that choice asks. (A row's own: rows weigh the same keys differently.)
     constexpr int R = C::RB * C::LR;
     auto row_of = [&](int i) { return NB == 1 ? tq : 8 * (i / 2) + 2 * tq + i % 2; };
-    float m[R], thr[R], ls[R], z[R][NG], oacc[C::MT][C::RB][4];
+    float nm[R], lw[R], thr[R], ls[R], z[R][NG], oacc[C::MT][C::RB][4];
     // (four groups: their sums are read at each chunk, from L1)
     const float *qx = reinterpret_cast<const float *>(qsrc + C::QF);
     float fc[R], qsum[R][NG < 4 ? NG : 1];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      m[i] = 0.f;           // (0 while thr is -inf)
+      nm[i] = 0.f;          // lw - m (m = 0 while thr is -inf)
+      lw[i] = 0.f;
       thr[i] = -INFINITY;   // raw score past which m is raised
       ls[i] = 0.f;
       fc[i] = mine ? __ldg(qx + row_of(i)) : 1.f;
@@ -440,8 +450,8 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
       for (int b = 0; b < C::RB; ++b)
 #pragma unroll
         for (int i = 0; i < 4; ++i) oacc[mt][b][i] = 0.f;
-    float wsc = 1.f;       // power of two: the value product's weights are p s wsc
-    float s_most = 0.f;    // scales up to this keep p s wsc below fp16's range
+    float s_top = 0.f;     // the largest scale so far
+    float s_most = 0.f;    // scales up to this keep p s 2^lw below fp16's range in every row
     // rows gq and gq + 8 of a tile's token operand; the tokens of the value product's
     // columns 2 tq, 2 tq + 1 (and + 8) are then ta, tb (and + 8)
     const int tA = gq ^ ((gq >> 1) & 1), tB = tA + 8;
@@ -574,7 +584,7 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
         for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int gg = 0; gg < NG; ++gg)
-            smax = fmaxf(smax, fmaxf(half_lo(vA[x][gg]), half_lo(vB[x][gg])));
+            smax = fmaxf(smax, fmaxf(fabsf(half_lo(vA[x][gg])), fabsf(half_lo(vB[x][gg]))));
         bool raise = smax > s_most;
         float top[R];
 #pragma unroll
@@ -585,39 +595,59 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
         if (__any_sync(0xFFFFFFFFu, raise)) {
           float fac[R];
 #pragma unroll
+          for (int o = 4; o < 32; o <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xFFFFFFFFu, smax, o));
+          const bool none = s_top == 0.f;  // (all weights so far are 0)
+          s_top = fmaxf(s_top, fminf(smax, 65504.f));
+          // 5 - floor(log2 s_top); as long as all scales are 0, no weight needs a range
+          const float least = s_top == 0.f ? 0.f : float(132 - int(__float_as_uint(s_top) >> 23));
+          s_most = s_top == 0.f ? 0.f : INFINITY;
+#pragma unroll
           for (int i = 0; i < R; ++i) {
             float x = top[i];
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
             x *= fc[i];
-            fac[i] = 1.f;
+            float now = lw[i] - nm[i], most = kMaxLw;  // m; what lw may be
             if (thr[i] == -INFINITY) {  // nothing but NaN so far, if anything
-              if (x > -INFINITY) m[i] = x, thr[i] = (x + 8.f) / fc[i];
-            } else if (x > m[i]) {
-              fac[i] = ex2(m[i] - x);
-              m[i] = x;
-              thr[i] = (x + 8.f) / fc[i];
+              if (x > -INFINITY) now = x;
+            } else {
+              // (weights so far, brought to the new m, need no more than they have)
+              const float rise = fmaxf(x - now, 0.f);
+              if (!none) most = fminf(most, lw[i] + rise);
+              now = fmaxf(x, now);
             }
+            const bool any = thr[i] != -INFINITY || x > -INFINITY;
+            float ps = 0.f;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                float big = 0.f;
+#pragma unroll
+                for (int gg = 0; gg < NG; ++gg) big = fmaxf(big, fabsf(half_lo(y ? vB[t][gg] : vA[t][gg])));
+                ps = fmaxf(ps, big * ex2(fmaf(sc[t][i][y], fc[i], -now)));
+              }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) ps = fmaxf(ps, __shfl_xor_sync(0xFFFFFFFFu, ps, o));
+            float l = lw[i];
+            if (s_top != 0.f) {
+              l = any ? fmaxf(least, fminf(most, -3.f - lg2(ps))) : least;
+              s_most = fminf(s_most, ex2(7.f - l));
+            }
+            const float n = l - now;
+            fac[i] = thr[i] == -INFINITY ? 1.f : ex2(n - nm[i]);
+            if (any) thr[i] = (now + 8.f) / fc[i];
+            nm[i] = n;
+            lw[i] = l;
             ls[i] *= fac[i];
 #pragma unroll
             for (int gg = 0; gg < NG; ++gg) z[i][gg] *= fac[i];
-          }
-          float ratio = 1.f;
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xFFFFFFFFu, smax, o));
-          if (smax > s_most) {  // bring smax * wsc to [32, 64); up to 128 is let pass
-            const uint32_t ex = (__float_as_uint(smax) >> 23) & 255u;
-            const float ns = __uint_as_float((254u + 5u - ex) << 23);
-            ratio = s_most == 0.f ? 1.f : ns / wsc;  // (no scale so far: oacc is 0)
-            wsc = ns;
-            s_most = 128.f / ns;
           }
 #pragma unroll
           for (int mt = 0; mt < C::MT; ++mt)
 #pragma unroll
             for (int b = 0; b < C::RB; ++b) {
-              const float fa = fac[NB == 1 ? 0 : 2 * b] * ratio;
-              const float fb = fac[NB == 1 ? 0 : 2 * b + 1] * ratio;
+              const float fa = fac[NB == 1 ? 0 : 2 * b], fb = fac[NB == 1 ? 0 : 2 * b + 1];
               oacc[mt][b][0] *= fa, oacc[mt][b][1] *= fb;
               oacc[mt][b][2] *= fa, oacc[mt][b][3] *= fb;
             }
@@ -627,15 +657,15 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
           float p[R][2];
 #pragma unroll
           for (int i = 0; i < R; ++i) {
-            p[i][0] = ex2(fmaf(sc[x][i][0], fc[i], -m[i]));
-            p[i][1] = ex2(fmaf(sc[x][i][1], fc[i], -m[i]));
+            p[i][0] = ex2(fmaf(sc[x][i][0], fc[i], nm[i]));
+            p[i][1] = ex2(fmaf(sc[x][i][1], fc[i], nm[i]));
             ls[i] += p[i][0] + p[i][1];
           }
           // weights of the value product per group, as its fragments
           uint32_t pf[NG][C::RB][2];
 #pragma unroll
           for (int gg = 0; gg < NG; ++gg) {
-            const float sA = half_lo(vA[x][gg]) * wsc, sB = half_lo(vB[x][gg]) * wsc;
+            const float sA = half_lo(vA[x][gg]), sB = half_lo(vB[x][gg]);
             const float zA = zero8(vA[x][gg]), zB = zero8(vB[x][gg]);
             float w[R][2];
 #pragma unroll
@@ -696,7 +726,7 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
         for (int gg = 0; gg < NG; ++gg) z[i][gg] += __shfl_xor_sync(0xFFFFFFFFu, z[i][gg], o);
       }
     }
-    const float up = 8.f / wsc;
+    constexpr float up = 8.f;
     // channels 32 blk + 4 gq .. + 3 of row row_of(i)
     auto out4 = [&](int blk, int i) {
       const float zz = 8.f * z[i][blk * 32 / G];
@@ -716,7 +746,7 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
         if (row >= s.nc) continue;
         if (gq == 0)
           *reinterpret_cast<float2 *>(rec + row * (4 + D)) =
-              make_float2(thr[i] == -INFINITY ? -INFINITY : m[i], ls[i]);
+              make_float2(thr[i] == -INFINITY ? -INFINITY : -nm[i], ls[i]);
 #pragma unroll
         for (int blk = 0; blk < C::W; ++blk)
           *reinterpret_cast<float4 *>(rec + row * (4 + D) + 4 + 32 * blk + 4 * gq) = out4(blk, i);
@@ -730,7 +760,7 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
 #pragma unroll
     for (int i = 0; i < R; ++i)
       if (gq == 0)
-        ml[warp * COLS + row_of(i)] = make_float2(thr[i] == -INFINITY ? -INFINITY : m[i], ls[i]);
+        ml[warp * COLS + row_of(i)] = make_float2(thr[i] == -INFINITY ? -INFINITY : -nm[i], ls[i]);
 #pragma unroll
     for (int c0 = 0; c0 < COLS; c0 += C::MC) {
       __syncthreads();  // the ring, and the rows before, are read

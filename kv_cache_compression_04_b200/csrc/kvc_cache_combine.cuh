@@ -14,6 +14,14 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The weights' common factor is 2^kMaxLw at most: sums of 2^31 weights of up to
+// 2^(kMaxLw + 8) stay in fp32's range.
+constexpr float kMaxLw = 60.f;
 __device__ __forceinline__ float half_lo(uint32_t m) {
   return __half2float(__ushort_as_half(uint16_t(m)));
 }

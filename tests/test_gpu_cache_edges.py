@@ -215,3 +215,43 @@ def test_lse_does_not_depend_on_values(d, g, asked, at):
     # (the weights' common power of two may differ: one rounding of a sum of a few units, and exp2's)
     assert (lse - want).abs().max() <= 2.0 ** -18
     assert torch.isfinite(out[0, ~see]).all() and torch.isfinite(fine).all()
+
+
+def ranged(kind, n, d, rng):
+    """Keys along one direction u, whose scores against u-like queries are `score` (times
+    the softmax's scale), and values of very different sizes."""
+    u = rng.standard_normal(d)
+    score, size = rng.uniform(-2, 2, n), np.full(n, 2.0 ** -13)
+    if kind == "first" or kind == "last":  # a huge value of no weight, before or after the others
+        i = 1 if kind == "first" else n - 2
+        score[i], size[i] = -60, 2.0 ** 12
+    elif kind == "slight":                 # whose weight makes it count as much as another
+        score[n // 2], size[n // 2] = -16, 2.0 ** 12
+    elif kind == "rising":                 # scores rise by 2^90 while sizes fall
+        score, size = np.linspace(-32, 32, n), 2.0 ** np.linspace(12, -13, n)
+    elif kind == "falling":
+        score, size = np.linspace(32, -32, n), 2.0 ** np.linspace(-13, 12, n)
+    elif kind == "mixed":
+        score, size = rng.uniform(-40, 8, n), 2.0 ** rng.uniform(-13, 12, n)
+    k = score[:, None] * u / (u @ u) * d ** 0.5
+    return u, k, size[:, None] * rng.standard_normal((n, d))
+
+
+@pytest.mark.parametrize("kind", ["first", "last", "slight", "rising", "falling", "mixed"])
+@pytest.mark.parametrize("d,g,qpk,asked,window", [
+    (128, 128, 4, 1, 0), (128, 32, 8, 1, 0), (64, 32, 7, 1, 0), (128, 64, 4, 4, 70), (64, 64, 8, 2, 0)])
+@pytest.mark.parametrize("n", [130, 700])
+def test_values_of_very_different_sizes(kind, d, g, qpk, asked, window, n):
+    """Scales of visible values up to 2^25 apart, with any weights, cost no precision: the
+    same bound as everywhere."""
+    rng = np.random.default_rng(n)
+    c = make(d, g, 1, 1, n // 16 + 2, 16)
+    u, k, v = ranged(kind, n, d, rng)
+    c.write(ref.bf16(k)[None, :, None].cuda(), ref.bf16(v)[None, :, None].cuda(), torch.arange(n, device="cuda"))
+    q = torch.from_numpy(u + 0.02 * rng.standard_normal((1, asked, qpk, d))).to(torch.bfloat16).cuda()
+    out = torch.empty_like(q)
+    c.attend(q, torch.arange(n // 16 + 1, dtype=torch.int32, device="cuda")[None], dev([n]), out=out,
+             q_starts=dev([0, asked]), max_q=asked, window=window)
+    c.check()
+    lim = [(max(0, n - asked + i + 1 - window) if window else 0, n - asked + i + 1) for i in range(asked)]
+    close(c, np.arange(n), q, out, qpk, lim, d ** -0.5, torch.bfloat16)

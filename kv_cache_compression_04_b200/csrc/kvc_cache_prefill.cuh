@@ -478,7 +478,7 @@ __device__ __forceinline__ void pf_unpack(const CacheAttnArgs &a, uint8_t *smem,
       uint8_t *kb = smem + C::k + buf * C::KBUF, *vb = smem + C::v + buf * C::KBUF;
       float *meta = reinterpret_cast<float *>(smem + C::meta) + buf * C::MW * NK;
       uint32_t most = 0;
-      uint32_t odd = 0;  // bit 0: a key that is not there, bit 1: a value that is not finite
+      bool gone = false, odd = false;  // a key that is not there, a value that is not finite
 #pragma unroll
       for (int x = 0; x < RX; ++x) {
         const uint32_t row = r0 + 32 * x, sw = row & 7;
@@ -558,14 +558,17 @@ __device__ __forceinline__ void pf_unpack(const CacheAttnArgs &a, uint8_t *smem,
           meta[2 * NG * NK + row] = bad ? -0.f : scale;
           meta[(2 * NG + 1) * NK + row] = bias;
         }
-        odd |= (w.in[x] ? 0u : 1u) | (bad ? 2u : 0u);
+        gone |= !w.in[x];
+        odd |= bad;
         most = max(most, __float_as_uint(scale));
       }
       most = __reduce_max_sync(0xFFFFFFFFu, most);
-      odd = __reduce_or_sync(0xFFFFFFFFu, odd);
+      uint32_t odds = 0;  // bit 0: some key is not there, bit 1: some value is not finite
+      if (__any_sync(0xFFFFFFFFu, gone || odd))
+        odds = (__any_sync(0xFFFFFFFFu, gone) ? 1u : 0u) | (__any_sync(0xFFFFFFFFu, odd) ? 2u : 0u);
       if (lane == 0) {
         reinterpret_cast<uint32_t *>(smem + C::wmax)[buf * 4 + warp] = most;
-        reinterpret_cast<uint32_t *>(smem + C::wodd)[buf * 4 + warp] = odd;
+        reinterpret_cast<uint32_t *>(smem + C::wodd)[buf * 4 + warp] = odds;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -812,9 +815,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       tm_fence_before();  // (the segment before has been read)
       __syncwarp();
       if (lane == 0) mbar_arrive(qready);
-      // Running state as in kvc_cache_attend.cuh: nm = -m (base 2, and - log2 of the
-      // values' common exponent: weights times 2^(a value's e) reach up to 2^15).
-      float nm = 0.f, mt = 0.f, thr = -INFINITY, l = 0.f, lw = 0.f, v_most = 0.f;
+      // Running state as in kvc_cache_attend.cuh, with 2^(a value's e) for its scale s: weights
+      // 2^(nm + score + e) reach up to 2^15; nm = lw - m. lw is chosen from the tile's e and the
+      // row's weights when m rises or a larger e comes.
+      float nm = 0.f, thr = -INFINITY, l = 0.f, lw = 0.f, v_most = 0.f;
       float *taint = reinterpret_cast<float *>(smem + C::taint) + which * kPfRows + row;
       *taint = 0.f;  // NaN once the row has seen a value that is not finite
 
@@ -855,12 +859,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         const uint4 odd = *reinterpret_cast<const uint4 *>(smem + C::wodd + buf * 16);
         const uint32_t odds = odd.x | odd.y | odd.z | odd.w;
-        if (odds & 2u) {  // values that are not finite: out is NaN for the rows that see them
+        if (odds || t0 < s.all_lo || uint32_t(t0) + NK > uint32_t(s.all_hi)) {
+          if (odds & 2u) {  // values that are not finite: out is NaN for the rows that see them
 #pragma unroll 1
-          for (int x = max(lo - t0, 0); x < min(hi - t0, NK); ++x)
-            if (__float_as_uint(meta[2 * NG * NK + x]) == 0x80000000u) *taint = __uint_as_float(0x7FFFFFFFu);
-        }
-        if ((odds & 1u) || t0 < s.all_lo || t0 > s.all_hi - NK) {
+            for (int x = max(lo - t0, 0); x < min(hi - t0, NK); ++x)
+              if (__float_as_uint(meta[2 * NG * NK + x]) == 0x80000000u) *taint = __uint_as_float(0x7FFFFFFFu);
+          }
 #pragma unroll
           for (int x = 0; x < NK; ++x) {
             const int32_t t = t0 + x;
@@ -877,24 +881,47 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
         const float4 wm = *reinterpret_cast<const float4 *>(smem + C::wmax + buf * 16);
         const float vm = fmaxf(fmaxf(wm.x, wm.y), fmaxf(wm.z, wm.w));
-        if (__any_sync(0xFFFFFFFFu, top > thr) || vm > v_most) {
-          float fac = 1.f;
+        if (__any_sync(0xFFFFFFFFu, top > thr || vm > v_most)) {
+          const float x = top * fc;
+          float now = lw - nm, most = kMaxLw;  // m; what lw may be
           if (thr == -INFINITY) {  // nothing but NaN so far, if anything
-            if (top > -INFINITY) mt = top * fc, thr = (mt + 8.f) / fc;
-          } else if (top > thr) {
-            const float x = top * fc;
-            fac = ex2(mt - x);
-            mt = x;
-            thr = (x + 8.f) / fc;
+            if (top > -INFINITY) now = x;
+          } else {
+            const float rise = top > thr ? x - now : 0.f;
+            if (v_most != 0.f) most = fminf(most, lw + rise);
+            now += rise;
           }
-          if (vm > v_most) {  // bring vm * 2^lw to 2^5; up to 2^7 is let pass
-            const int ex = int(__float_as_uint(vm) >> 23) - 127;
-            const float nl = float(5 - ex);
-            fac *= ex2(nl - lw);
-            lw = nl;
-            v_most = ex2(float(ex + 2));
+          const bool any = thr != -INFINITY || top > -INFINITY;
+          // the smallest e but zeros' (0: zeros alone)
+          const uint32_t *vb = reinterpret_cast<const uint32_t *>(meta) + 2 * NG * NK;
+          uint32_t low = (vb[lane] & 0x7FFFFFFFu) - 1u;
+          if constexpr (NK == 64) low = min(low, (vb[lane + 32] & 0x7FFFFFFFu) - 1u);
+          low = (__reduce_min_sync(0xFFFFFFFFu, low) + 1u) >> 23;
+          float lnew = lw;
+          if (vm != 0.f || v_most != 0.f) {
+            const float least = vm == 0.f ? -INFINITY : float(132 - int(__float_as_uint(vm) >> 23));  // 5 - e
+            // m + log2 of the largest weight; where the e are so much alike that `least` is
+            // the larger choice for sure, the largest score with the smallest e does
+            float big = x + float(int(low) - 127);
+            if (low == 0u || now - 3.f - big > least) {
+              big = -INFINITY;
+#pragma unroll
+              for (int y = 0; y < NK; y += 4) {
+                const uint4 ev = *reinterpret_cast<const uint4 *>(meta + 2 * NG * NK + y);
+                auto at = [&](float x, uint32_t u) {  // x fc + e (zeros: -127)
+                  return fmaf(x, fc, __uint_as_float(((u >> 23) & 255u) | 0x4B000000u) - 8388735.f);
+                };
+                big = max3(max3(big, at(sc[y], ev.x), at(sc[y + 1], ev.y)), at(sc[y + 2], ev.z), at(sc[y + 3], ev.w));
+              }
+            }
+            if (any) lnew = fmaxf(least, fminf(most, now - 3.f - big));
+            else if (vm != 0.f) lnew = least;
+            v_most = ex2(7.f - lnew);
           }
-          nm = lw - mt;
+          const float fac = thr == -INFINITY ? 1.f : ex2(lnew - now - nm);
+          if (any) thr = (now + 8.f) / fc;
+          nm = lnew - now;
+          lw = lnew;
           l *= fac;
           if (i > 1) {  // this softmax's last values are in
             pf_wait(pv + (j - 2) % kPfStages, ((j - 2) / kPfStages) & 1u, dead, a.status);
@@ -944,7 +971,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       j0 += s.tiles;
       pf_wait(pv + (j0 - 1) % kPfStages, ((j0 - 1) / kPfStages) & 1u, dead, a.status);
       tm_fence_after();
-      fin[which * kPfRows + row] = make_float2(thr == -INFINITY ? -INFINITY : mt - lw, l);
+      fin[which * kPfRows + row] = make_float2(thr == -INFINITY ? -INFINITY : -nm, l);
       named_bar_sync(1, kPfSoft);
       const float2 mine[2] = {fin[row], fin[kPfRows + row]};
       const float m = fmaxf(mine[0].x, mine[1].x);

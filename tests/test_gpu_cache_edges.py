@@ -239,7 +239,8 @@ def ranged(kind, n, d, rng):
 
 @pytest.mark.parametrize("kind", ["first", "last", "slight", "rising", "falling", "mixed"])
 @pytest.mark.parametrize("d,g,qpk,asked,window", [
-    (128, 128, 4, 1, 0), (128, 32, 8, 1, 0), (64, 32, 7, 1, 0), (128, 64, 4, 4, 70), (64, 64, 8, 2, 0)])
+    (128, 128, 4, 1, 0), (128, 32, 8, 1, 0), (64, 32, 7, 1, 0), (128, 64, 4, 4, 70), (64, 64, 8, 2, 0),
+    (128, 128, 4, 30, 0), (128, 64, 8, 20, 0), (128, 32, 4, 40, 90), (64, 64, 4, 40, 0), (64, 32, 64, 1, 0)])
 @pytest.mark.parametrize("n", [130, 700])
 def test_values_of_very_different_sizes(kind, d, g, qpk, asked, window, n):
     """Scales of visible values up to 2^25 apart, with any weights, cost no precision: the
@@ -255,3 +256,24 @@ def test_values_of_very_different_sizes(kind, d, g, qpk, asked, window, n):
     c.check()
     lim = [(max(0, n - asked + i + 1 - window) if window else 0, n - asked + i + 1) for i in range(asked)]
     close(c, np.arange(n), q, out, qpk, lim, d ** -0.5, torch.bfloat16)
+
+
+@pytest.mark.parametrize("d,g", [(128, 128), (128, 32), (64, 64)])
+@pytest.mark.parametrize("asked", [2, 6, 50])
+def test_zero_values_beside_one_that_is_not_finite(d, g, asked):
+    """The last tiles hold zeros and, in the last token, a value stored as NaN: the queries
+    before it get what the other values weigh."""
+    n, qpk = 164, 4
+    c = make(d, g, 1, 1, 12, 16)
+    k, v = rows(1, n, 1, d)
+    v[:, 100:] = 0
+    v[0, n - 1, 0, 3] = float("nan")
+    c.write(k, v, torch.arange(n, device="cuda"))
+    assert status_of(c) == kvc.KVC_ERR_NONFINITE
+    q = torch.randn(1, asked, qpk, d, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    out = c.attend(q.cuda(), torch.arange(11, dtype=torch.int32, device="cuda")[None], dev([n]),
+                   q_starts=dev([0, asked]), max_q=asked)
+    c.check()
+    assert torch.isnan(out[0, -1]).all()
+    close(c, np.arange(n), q[:, :-1], out[:, :-1], qpk, [(0, n - asked + i + 1) for i in range(asked - 1)],
+          d ** -0.5, torch.bfloat16)

@@ -802,6 +802,7 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
 template <int C_, int CW>
 struct DecodeRecords {
   static constexpr int COLS = C_;
+  static constexpr bool kWide = true;
   uint64_t unit = 0;
   uint32_t row = 0, nrec = 0, n0 = 0, s0 = 0, b0 = 0, b1 = 0;
   __device__ __forceinline__ DecodeRecords(const CacheAttnArgs &a, uint32_t grid, const ReqShape &q,

@@ -221,16 +221,18 @@ __global__ void __launch_bounds__(WPR == 1 ? 128 : WPR * 32)
 }
 
 
-// dtype, and whether records are spread wide (eight warps a row).
+// dtype, and whether records are spread wide (eight warps a row; where At asks for it).
 template <int D, class At>
 cudaError_t launch_combine(int dtype, bool wide, const CacheAttnArgs &a, uint32_t grid,
                            cudaStream_t st) {
   const uint64_t rows = uint64_t(a.c.layers) * a.q_tokens * a.c.heads * a.qpk;
   const uint64_t cg = wide ? rows : (rows + 3) / 4;  // (below 2^31: checked before the first kernel)
-  auto ck = dtype == KVC_BF16 ? (wide ? cache_combine_kernel<D, At, KVC_BF16, 8>
-                                      : cache_combine_kernel<D, At, KVC_BF16, 1>)
-                              : (wide ? cache_combine_kernel<D, At, KVC_FP16, 8>
-                                      : cache_combine_kernel<D, At, KVC_FP16, 1>);
+  auto ck = dtype == KVC_BF16 ? cache_combine_kernel<D, At, KVC_BF16, 1>
+                              : cache_combine_kernel<D, At, KVC_FP16, 1>;
+  if constexpr (At::kWide)
+    if (wide)
+      ck = dtype == KVC_BF16 ? cache_combine_kernel<D, At, KVC_BF16, 8>
+                             : cache_combine_kernel<D, At, KVC_FP16, 8>;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned(cg));
   cfg.blockDim = dim3(wide ? 256 : 128);

@@ -718,7 +718,7 @@ __device__ __forceinline__ void pf_issue(const CacheAttnArgs &a, uint8_t *smem, 
 
 template <int D, int G>
 __global__ void __launch_bounds__(kPfThreads, 1)
-    cache_prefill_kernel(const __grid_constant__ CacheAttnArgs a, const int dtype) {
+    cache_prefill_kernel(const __grid_constant__ CacheAttnArgs a) {
   using C = PfCfg<D, G>;
   constexpr int NG = C::NG, NK = C::NK, W = C::W;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -1023,6 +1023,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 // A row's records: one per CTA that has some of the block's tiles.
 struct PrefillRecords {
   static constexpr int COLS = kPfRows;
+  static constexpr bool kWide = false;  // (a block has a record per CTA that it was cut for: few)
   uint64_t unit = 0;
   uint32_t row = 0, nrec = 0, g0 = 0;
   __device__ __forceinline__ PrefillRecords(const CacheAttnArgs &a, uint32_t grid, const ReqShape &q,
@@ -1063,7 +1064,7 @@ cudaError_t cache_prefill_t(int dtype, const CacheAttnArgs &a, int sms, cudaStre
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, k, a, dtype);
+  e = cudaLaunchKernelEx(&cfg, k, a);
   if (e != cudaSuccess) return e;
   return launch_combine<D, PrefillRecords>(dtype, false, a, grid, st);
 }

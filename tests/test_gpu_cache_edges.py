@@ -277,3 +277,30 @@ def test_zero_values_beside_one_that_is_not_finite(d, g, asked):
     assert torch.isnan(out[0, -1]).all()
     close(c, np.arange(n), q[:, :-1], out[:, :-1], qpk, [(0, n - asked + i + 1) for i in range(asked - 1)],
           d ** -0.5, torch.bfloat16)
+
+
+@pytest.mark.parametrize("kind", ["first", "last", "slight", "rising", "falling", "mixed"])
+@pytest.mark.parametrize("d,g,qpk,asked", [(128, 128, 4, 1), (128, 32, 8, 1), (64, 64, 7, 2), (128, 64, 4, 20),
+                                           (64, 32, 4, 30)])
+def test_values_of_very_different_sizes_in_long_segments(kind, d, g, qpk, asked):
+    """The same where a warp (or block) goes through all of a request's keys itself: many
+    requests and heads that share them."""
+    n, L, H, R = 700, 2, 16, 24
+    rng = np.random.default_rng(n + d + g)
+    c = make(d, g, L, H, n // 16 + 2, 16)
+    u, k, v = ranged(kind, n, d, rng)
+    c.write(*(ref.bf16(x)[None, :, None].expand(L, n, H, d).contiguous().cuda() for x in (k, v)),
+            torch.arange(n, device="cuda"))
+    one = torch.from_numpy(u + 0.02 * rng.standard_normal((1, asked, qpk, d))).to(torch.bfloat16)
+    q = one.repeat(L, R, H, 1).cuda()
+    tab = torch.arange(n // 16 + 1, dtype=torch.int32, device="cuda").expand(R, -1)
+    out = c.attend(q, tab, dev([n] * R), q_starts=dev([asked * i for i in range(R + 1)]), max_q=asked)
+    c.check()
+    x, spread = (t[:1, :, :1] for t in cache_values(c, np.arange(n)))
+    o, _, mag, size = ref.attend(x, one.double().numpy(), qpk, d ** -0.5,
+                                 [(0, n - asked + i + 1) for i in range(asked)], spread)
+    ds = 2.0 ** -18 * size + 2.0 ** -20
+    tol = 2.0 ** -8 * np.abs(o) + (2 * ds + 2.0 ** -11)[..., None] * mag * 1.01 + 1e-7
+    got = out.double().cpu().numpy().reshape(L, R, asked, H, qpk, d)
+    bad = np.abs(got - o[0][None, None, :, None]) - tol[0][None, None, :, None]
+    assert (bad <= 0).all(), bad.max()

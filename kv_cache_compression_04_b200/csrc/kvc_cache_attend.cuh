@@ -24,9 +24,9 @@
 // either, the warp-level product is an emulation: 60% slower in all.) Queries are split
 // in fp16 hi + lo (22 bits). The eight columns are eight query rows, the score
 // product taking both parts into one sum; the value product's weights are rounded to
-// fp16 once (2^-12 relative at most, independent per key: no more than rounding the
-// output to fp16). Up to 4 rows, columns 2 i, 2 i + 1 are row i's two parts in both
-// products.
+// fp16 once (2^-11 relative at most, independent per key, and 2^-27 of the row's largest
+// weight for small ones: no more than rounding the output to fp16). Up to 4 rows, columns
+// 2 i, 2 i + 1 are row i's two parts in both products.
 //
 // Few query rows (queries x query heads per kv head) of a request, 16 at a time; many are
 // kvc_cache_prefill.cuh's (cache_few_rows).
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
     if (s.chunks == 0 && !one_unit) continue;
 
     // ---- the segment's chunks, copied ahead of their use (the unit's fragments are
-    // read from the workspace at each: they stay in L1, beside 16 warps' rings)
+    // read from the workspace at each: they stay in L1, beside 12 warps' rings)
     const uint32_t mine = s.chunks;
     const uint8_t *kbase = a.c.pool + int64_t(s.l) * a.c.s_l + int64_t(s.h) * a.c.s_h;
     const int32_t *table = a.page_table + int64_t(s.r) * a.pt_stride;
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
     // All sums hold p 2^lw, whose products with the values' scales s are the value product's
     // weights: fp16, so lw keeps them in its range. Of two choices a row takes the larger,
     //   5 - floor(log2 of the largest s so far): p s 2^lw < 2^14 for any p, and
-    //   -3 - log2 of the largest p s: where the largest s has little weight. (Without it one
+    //   kAimLw - log2 of the largest p s: where the largest s has little weight. (Without it one
     //   visible value of 2^20 times the others' scale and no weight pushed their weights into
     //   the subnormals: errors of 1.6e-3, at 2^24 of 0.11.)
     // The largest p s is looked for where lw is chosen anew, when m rises or a scale comes
@@ -601,42 +601,57 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
           // 5 - floor(log2 s_top); as long as all scales are 0, no weight needs a range
           const float least = s_top == 0.f ? 0.f : float(132 - int(__float_as_uint(s_top) >> 23));
           s_most = s_top == 0.f ? 0.f : INFINITY;
+          // the smallest scale but zeros: with it and the largest score, the largest p s need not
+          // be looked for where scales are much alike
+          uint32_t low = ~0u;
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int gg = 0; gg < NG; ++gg)
+              low = min(low, min((vA[x][gg] & 0x7FFFu) - 1u, (vB[x][gg] & 0x7FFFu) - 1u));
+          low = __reduce_min_sync(0xFFFFFFFFu, low) + 1u;
+          const float e_low = float(int(__float_as_uint(half_lo(low)) >> 23) - 127);
+          bool look = low == 0u;
+          float now[R];
 #pragma unroll
           for (int i = 0; i < R; ++i) {
             float x = top[i];
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
             x *= fc[i];
-            float now = lw[i] - nm[i], most = kMaxLw;  // m; what lw may be
-            if (thr[i] == -INFINITY) {  // nothing but NaN so far, if anything
-              if (x > -INFINITY) now = x;
-            } else {
+            const float was = lw[i] - nm[i];  // m
+            now[i] = thr[i] != -INFINITY ? fmaxf(x, was) : x > -INFINITY ? x : was;
+            look |= now[i] + kAimLw - (x + e_low) > least;
+            top[i] = x;
+          }
+          look = __any_sync(0xFFFFFFFFu, look);
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const float was = lw[i] - nm[i];
+            const bool any = thr[i] != -INFINITY || top[i] > -INFINITY;
+            float l = least;
+            if (look) {
+              float ps = 0.f;
+#pragma unroll
+              for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  float big = 0.f;
+#pragma unroll
+                  for (int gg = 0; gg < NG; ++gg) big = fmaxf(big, fabsf(half_lo(y ? vB[t][gg] : vA[t][gg])));
+                  ps = fmaxf(ps, big * ex2(fmaf(sc[t][i][y], fc[i], -now[i])));
+                }
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) ps = fmaxf(ps, __shfl_xor_sync(0xFFFFFFFFu, ps, o));
               // (weights so far, brought to the new m, need no more than they have)
-              const float rise = fmaxf(x - now, 0.f);
-              if (!none) most = fminf(most, lw[i] + rise);
-              now = fmaxf(x, now);
+              const float most = thr[i] == -INFINITY || none ? kMaxLw : fminf(kMaxLw, lw[i] + (now[i] - was));
+              if (any) l = fmaxf(least, fminf(most, kAimLw - lg2(ps)));
             }
-            const bool any = thr[i] != -INFINITY || x > -INFINITY;
-            float ps = 0.f;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                float big = 0.f;
-#pragma unroll
-                for (int gg = 0; gg < NG; ++gg) big = fmaxf(big, fabsf(half_lo(y ? vB[t][gg] : vA[t][gg])));
-                ps = fmaxf(ps, big * ex2(fmaf(sc[t][i][y], fc[i], -now)));
-              }
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) ps = fmaxf(ps, __shfl_xor_sync(0xFFFFFFFFu, ps, o));
-            float l = lw[i];
-            if (s_top != 0.f) {
-              l = any ? fmaxf(least, fminf(most, -3.f - lg2(ps))) : least;
-              s_most = fminf(s_most, ex2(7.f - l));
-            }
-            const float n = l - now;
+            if (s_top == 0.f) l = lw[i];
+            else s_most = fminf(s_most, ex2(7.f - l));
+            const float n = l == lw[i] && now[i] == was ? nm[i] : l - now[i];
             fac[i] = thr[i] == -INFINITY ? 1.f : ex2(n - nm[i]);
-            if (any) thr[i] = (now + 8.f) / fc[i];
+            if (any) thr[i] = (now[i] + 8.f) / fc[i];
             nm[i] = n;
             lw[i] = l;
             ls[i] *= fac[i];

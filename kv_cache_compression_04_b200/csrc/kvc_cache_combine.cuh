@@ -1,4 +1,4 @@
-// What the two forms of the cache's attention share (kvc_cache_attend.cuh, up to 16 query
+// What the two forms of the cache's attention share (kvc_cache_attend.cuh, few query
 // rows per request; kvc_cache_prefill.cuh, more): the requests' numbers, searches in
 // prefixes, and the kernel that merges a row's records.
 #pragma once
@@ -22,6 +22,10 @@ __device__ __forceinline__ float lg2(float x) {
 // The weights' common factor is 2^kMaxLw at most: sums of 2^31 weights of up to
 // 2^(kMaxLw + 8) stay in fp32's range.
 constexpr float kMaxLw = 60.f;
+// log2 of what a row's largest weight is brought to at least: the rest are kept to 2^-25, so
+// that even 2^15 of them, all rounded the same way, are off by 2^-12 of it. (Each power of two
+// more lets scales of half the size ask for the slow choice of the factor.)
+constexpr float kAimLw = 2.f;
 __device__ __forceinline__ float half_lo(uint32_t m) {
   return __half2float(__ushort_as_half(uint16_t(m)));
 }

@@ -15,12 +15,13 @@
 //         rounds. (With z + 8 s and n - 8 the sum was rounded before it: the same for all
 //         channels of a group, which the inverse transform puts into one.)
 // Floor per 128 x 64 tile pair at d = 128: 3 x 256 cycles of the tensor cores (hi and
-// lo parts, values). Measured: 1024 queries x 32 heads over 9216 keys in 255 us (574
-// TFLOP/s of the two products counted once), about 1750 cycles a tile, of which the
-// tensor cores are active for 768. A softmax works for most of its two tiles' time (two
-// softmax and two unpacking warps share an SM quarter's issue, 58% of it used), and
-// shared memory serves 850 wavefronts and the products' operands a tile. With two groups
-// 316 us, with four 447 us (two tiles' scores fit, and more fused multiplies).
+// lo parts, values). Measured: 1024 queries x 32 heads over 9216 keys in 255 us at 1965 MHz
+// (574 TFLOP/s of the two products counted once) and in 280 at the 1815 MHz at which the
+// power cap holds a loop of such calls; 1660 cycles a tile, of which the
+// tensor cores are active for 770. A softmax works for most of its two tiles' time (two
+// softmax and two unpacking warps share an SM quarter's issue, 62% of it used), and
+// shared memory serves 840 wavefronts and the products' operands a tile. With two groups
+// 324 us, with four 460 us (two tiles' scores fit, and more fused multiplies).
 //
 // Warps 0..3 do the even tiles' softmax, 4..7 the odd ones', a thread per row with a
 // maximum, a sum and an output accumulator of its own: the two never wait for each other,
@@ -49,7 +50,7 @@ constexpr int kPfSoft = 256, kPfUnpack = 256, kPfThreads = kPfSoft + kPfUnpack +
 constexpr int kPfSoftRegs = 136, kPfUnpackRegs = 72, kPfIssueRegs = 64;
 constexpr uint32_t kPfStages = 4;
 // A segment's fixed work (queries, first tiles, record) in tiles. 2048 queries over their
-// own keys with 3, 8, 10, 16: 213, 173, 167, 171 us; 1024 over 9216: 270, 269, 268, 271.
+// own keys with 3, 8, 10, 16: 213, 176, 169, 169 us; 1024 over 9216: 257, 255, 255, 260.
 constexpr uint32_t kPfLead = 10;
 
 template <int D, int G>
@@ -883,7 +884,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const float vm = fmaxf(fmaxf(wm.x, wm.y), fmaxf(wm.z, wm.w));
         if (__any_sync(0xFFFFFFFFu, top > thr || vm > v_most)) {
           const float x = top * fc;
-          float now = lw - nm, most = kMaxLw;  // m; what lw may be
+          const float was = lw - nm;
+          float now = was, most = kMaxLw;  // m; what lw may be
           if (thr == -INFINITY) {  // nothing but NaN so far, if anything
             if (top > -INFINITY) now = x;
           } else {
@@ -903,7 +905,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             // m + log2 of the largest weight; where the e are so much alike that `least` is
             // the larger choice for sure, the largest score with the smallest e does
             float big = x + float(int(low) - 127);
-            if (low == 0u || now - 3.f - big > least) {
+            if (low == 0u || now + kAimLw - big > least) {
               big = -INFINITY;
 #pragma unroll
               for (int y = 0; y < NK; y += 4) {
@@ -914,16 +916,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 big = max3(max3(big, at(sc[y], ev.x), at(sc[y + 1], ev.y)), at(sc[y + 2], ev.z), at(sc[y + 3], ev.w));
               }
             }
-            if (any) lnew = fmaxf(least, fminf(most, now - 3.f - big));
+            if (any) lnew = fmaxf(least, fminf(most, now + kAimLw - big));
             else if (vm != 0.f) lnew = least;
             v_most = ex2(7.f - lnew);
           }
-          const float fac = thr == -INFINITY ? 1.f : ex2(lnew - now - nm);
+          const float n = lnew == lw && now == was ? nm : lnew - now;
+          const float fac = thr == -INFINITY ? 1.f : ex2(n - nm);
           if (any) thr = (now + 8.f) / fc;
-          nm = lnew - now;
+          nm = n;
           lw = lnew;
           l *= fac;
-          if (i > 1) {  // this softmax's last values are in
+          if (i > 1 && __any_sync(0xFFFFFFFFu, fac != 1.f)) {  // this softmax's last values are in
             pf_wait(pv + (j - 2) % kPfStages, ((j - 2) / kPfStages) & 1u, dead, a.status);
             tm_fence_after();
             __syncwarp();

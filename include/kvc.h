@@ -507,7 +507,9 @@ uint64_t kvc_cache_stream_seed(const kvc_cache_desc *cache);
  * Query head j reads kv head j / q_per_kv:
  *   s_t = scale * q . k_t,  out = sum_t softmax(s)_t v_t,  lse = ln sum_t e^s_t
  * with k_t, v_t the stored vectors before kvc_cache_read's rounding. Scores and
- * sums are held in fp32, out is rounded once to dtype. A query that sees no key
+ * sums are held in fp32, out is rounded once to dtype; more than 4 query rows'
+ * weights, and for blocks of 128 the values, are rounded to fp16 for their
+ * product (each times a power of two that keeps it in range). A query that sees no key
  * gives zeros and lse -inf. Rows of q that no request names are left as they
  * were in out and lse; NaN and infinities in slots past a request's length are
  * never used; a visible value stored as NaN makes out NaN and leaves lse as it

@@ -8,6 +8,11 @@
 // A block's rows are 32 tokens apart by the token stride: 16-byte pieces go through
 // the warp's swizzled buffer, half a warp per row, the next block's while this one
 // is computed.
+//
+// Measured: 4096 tokens x 32 layers written in 145 us (0.72 of the copy rate), read in 153
+// (0.69). Neither unit is full: issue slots 63% used (written) and 66% (read), the integer
+// pipe 47% and 57%, DRAM 54% and 48%; the three warps of an SM quarter, all that 168 registers
+// a lane leave, spend their time on one another's instructions and on results of their own.
 #pragma once
 
 #include "kvc_cache_rows.cuh"

@@ -509,11 +509,11 @@ uint64_t kvc_cache_stream_seed(const kvc_cache_desc *cache);
  * with k_t, v_t the stored vectors before kvc_cache_read's rounding. Scores and
  * sums are held in fp32, out is rounded once to dtype; more than 4 query rows'
  * weights, and for blocks of 128 the values, are rounded to fp16 for their
- * product (each times a power of two that keeps it in range). A query that sees no key
- * gives zeros and lse -inf. Rows of q that no request names are left as they
- * were in out and lse; NaN and infinities in slots past a request's length are
- * never used; a visible value stored as NaN makes out NaN and leaves lse as it
- * is. A request whose q_starts or seq_lens is out of range (decreasing
+ * product (times a factor of the row's or key's own that keeps them in range). A
+ * query that sees no key gives zeros and lse -inf. Rows of q that no request
+ * names are left as they were in out and lse; NaN and infinities in slots past a
+ * request's length are never used; a visible value stored as NaN makes out NaN
+ * and leaves lse as it is. A request whose q_starts or seq_lens is out of range (decreasing
  * or outside [0, q_tokens]; more than max_q queries; a length below 0 or past
  * its row of the page table) sets KVC_ERR_CORRUPT and its rows are left as they
  * were (where q_starts decrease, the other requests' rows are unspecified); a

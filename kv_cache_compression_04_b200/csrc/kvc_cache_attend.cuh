@@ -24,7 +24,7 @@
 // either, the warp-level product is an emulation: 60% slower in all.) Queries are split
 // in fp16 hi + lo (22 bits). The eight columns are eight query rows, the score
 // product taking both parts into one sum; the value product's weights are rounded to
-// fp16 once (2^-11 relative at most, independent per key, and 2^-27 of the row's largest
+// fp16 once (2^-11 relative at most, independent per key, and 2^-30 of the row's largest
 // weight for small ones: no more than rounding the output to fp16). Up to 4 rows, columns
 // 2 i, 2 i + 1 are row i's two parts in both products.
 //
@@ -414,28 +414,18 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
     }
 
     // ---- running state of this lane's rows: LR per block, row (NB == 1 ? tq : 8 b +
-    // 2 tq + i). Scores are kept raw; their maximum m, in base 2, follows only jumps of
-    // more than 2^8 (weights p = 2^(score - m) reach 2^8; sums in fp32 lose nothing by it).
-    // All sums hold p 2^lw, whose products with the values' scales s are the value product's
-    // weights: fp16, so lw keeps them in its range. Of two choices a row takes the larger,
-    //   5 - floor(log2 of the largest s so far): p s 2^lw < 2^14 for any p, and
-    //   kAimLw - log2 of the largest p s: where the largest s has little weight. (Without it one
-    //   visible value of 2^20 times the others' scale and no weight pushed their weights into
-    //   the subnormals: errors of 1.6e-3, at 2^24 of 0.11.)
-    // The largest p s is looked for where lw is chosen anew, when m rises or a scale comes
-    // that p 2^8 could take past 2^15; between, lw stands, and it never comes down further
-    // than that choice asks. (A row's own: rows weigh the same keys differently.)
+    // 2 tq + i). Scores are kept raw; n (row_factor) is a row's own, as rows weigh the same
+    // keys differently.
     constexpr int R = C::RB * C::LR;
     auto row_of = [&](int i) { return NB == 1 ? tq : 8 * (i / 2) + 2 * tq + i % 2; };
-    float nm[R], lw[R], thr[R], ls[R], z[R][NG], oacc[C::MT][C::RB][4];
+    float nm[R], lim[R], ls[R], z[R][NG], oacc[C::MT][C::RB][4];
     // (four groups: their sums are read at each chunk, from L1)
     const float *qx = reinterpret_cast<const float *>(qsrc + C::QF);
     float fc[R], qsum[R][NG < 4 ? NG : 1];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      nm[i] = 0.f;          // lw - m (m = 0 while thr is -inf)
-      lw[i] = 0.f;
-      thr[i] = -INFINITY;   // raw score past which m is raised
+      nm[i] = 0.f;          // n
+      lim[i] = -INFINITY;   // most log2 p may be (-inf: no keys so far, or nothing but NaN)
       ls[i] = 0.f;
       fc[i] = mine ? __ldg(qx + row_of(i)) : 1.f;
 #pragma unroll
@@ -450,8 +440,6 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
       for (int b = 0; b < C::RB; ++b)
 #pragma unroll
         for (int i = 0; i < 4; ++i) oacc[mt][b][i] = 0.f;
-    float s_top = 0.f;     // the largest scale so far
-    float s_most = 0.f;    // scales up to this keep p s 2^lw below fp16's range in every row
     // rows gq and gq + 8 of a tile's token operand; the tokens of the value product's
     // columns 2 tq, 2 tq + 1 (and + 8) are then ta, tb (and + 8)
     const int tA = gq ^ ((gq >> 1) & 1), tB = tA + 8;
@@ -578,31 +566,27 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
             }
           }
         }
-        // New maximum or scale range?
+        // Could a weight pass its range?
         float smax = 0.f;
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int gg = 0; gg < NG; ++gg)
             smax = fmaxf(smax, fmaxf(fabsf(half_lo(vA[x][gg])), fabsf(half_lo(vB[x][gg]))));
-        bool raise = smax > s_most;
+        const float room = kWeightMost - 1.f - log2_floor(__float_as_uint(smax));
+        bool raise = false;
         float top[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           top[i] = fmaxf(fmaxf(sc[0][i][0], sc[0][i][1]), fmaxf(sc[1][i][0], sc[1][i][1]));
-          raise |= top[i] > thr[i];
+          raise |= fmaf(top[i], fc[i], nm[i]) > fminf(lim[i], room);
         }
         if (__any_sync(0xFFFFFFFFu, raise)) {
           float fac[R];
+          // The largest and the smallest scale but zeros: where they are alike, the largest score
+          // with the largest scale will do for the largest weight.
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xFFFFFFFFu, smax, o));
-          const bool none = s_top == 0.f;  // (all weights so far are 0)
-          s_top = fmaxf(s_top, fminf(smax, 65504.f));
-          // 5 - floor(log2 s_top); as long as all scales are 0, no weight needs a range
-          const float least = s_top == 0.f ? 0.f : float(132 - int(__float_as_uint(s_top) >> 23));
-          s_most = s_top == 0.f ? 0.f : INFINITY;
-          // the smallest scale but zeros: with it and the largest score, the largest p s need not
-          // be looked for where scales are much alike
           uint32_t low = ~0u;
 #pragma unroll
           for (int x = 0; x < 2; ++x)
@@ -610,26 +594,15 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
             for (int gg = 0; gg < NG; ++gg)
               low = min(low, min((vA[x][gg] & 0x7FFFu) - 1u, (vB[x][gg] & 0x7FFFu) - 1u));
           low = __reduce_min_sync(0xFFFFFFFFu, low) + 1u;
-          const float e_low = float(int(__float_as_uint(half_lo(low)) >> 23) - 127);
-          bool look = low == 0u;
-          float now[R];
+          const float e_top = log2_floor(__float_as_uint(fminf(smax, 65504.f)));
+          const bool look = low == 0u || e_top - log2_floor(__float_as_uint(half_lo(low))) > 3.f;
 #pragma unroll
           for (int i = 0; i < R; ++i) {
             float x = top[i];
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
             x *= fc[i];
-            const float was = lw[i] - nm[i];  // m
-            now[i] = thr[i] != -INFINITY ? fmaxf(x, was) : x > -INFINITY ? x : was;
-            look |= now[i] + kAimLw - (x + e_low) > least;
-            top[i] = x;
-          }
-          look = __any_sync(0xFFFFFFFFu, look);
-#pragma unroll
-          for (int i = 0; i < R; ++i) {
-            const float was = lw[i] - nm[i];
-            const bool any = thr[i] != -INFINITY || top[i] > -INFINITY;
-            float l = least;
+            float w = x + e_top + 1.f;
             if (look) {
               float ps = 0.f;
 #pragma unroll
@@ -639,21 +612,20 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
                   float big = 0.f;
 #pragma unroll
                   for (int gg = 0; gg < NG; ++gg) big = fmaxf(big, fabsf(half_lo(y ? vB[t][gg] : vA[t][gg])));
-                  ps = fmaxf(ps, big * ex2(fmaf(sc[t][i][y], fc[i], -now[i])));
+                  ps = fmaxf(ps, big * ex2(fmaf(sc[t][i][y], fc[i], -x)));
                 }
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) ps = fmaxf(ps, __shfl_xor_sync(0xFFFFFFFFu, ps, o));
-              // (weights so far, brought to the new m, need no more than they have)
-              const float most = thr[i] == -INFINITY || none ? kMaxLw : fminf(kMaxLw, lw[i] + (now[i] - was));
-              if (any) l = fmaxf(least, fminf(most, kAimLw - lg2(ps)));
+              w = x + lg2(ps);
             }
-            if (s_top == 0.f) l = lw[i];
-            else s_most = fminf(s_most, ex2(7.f - l));
-            const float n = l == lw[i] && now[i] == was ? nm[i] : l - now[i];
-            fac[i] = thr[i] == -INFINITY ? 1.f : ex2(n - nm[i]);
-            if (any) thr[i] = (now[i] + 8.f) / fc[i];
-            nm[i] = n;
-            lw[i] = l;
+            fac[i] = 1.f;
+            if (x > -INFINITY) {
+              const bool first = lim[i] == -INFINITY;
+              const float n = row_factor(nm[i], x, w, first);
+              if (!first) fac[i] = ex2(n - nm[i]);
+              nm[i] = n;
+              lim[i] = kPMost;
+            }
             ls[i] *= fac[i];
 #pragma unroll
             for (int gg = 0; gg < NG; ++gg) z[i][gg] *= fac[i];
@@ -761,7 +733,7 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
         if (row >= s.nc) continue;
         if (gq == 0)
           *reinterpret_cast<float2 *>(rec + row * (4 + D)) =
-              make_float2(thr[i] == -INFINITY ? -INFINITY : -nm[i], ls[i]);
+              make_float2(lim[i] == -INFINITY ? -INFINITY : -nm[i], ls[i]);
 #pragma unroll
         for (int blk = 0; blk < C::W; ++blk)
           *reinterpret_cast<float4 *>(rec + row * (4 + D) + 4 + 32 * blk + 4 * gq) = out4(blk, i);
@@ -775,7 +747,7 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
 #pragma unroll
     for (int i = 0; i < R; ++i)
       if (gq == 0)
-        ml[warp * COLS + row_of(i)] = make_float2(thr[i] == -INFINITY ? -INFINITY : -nm[i], ls[i]);
+        ml[warp * COLS + row_of(i)] = make_float2(lim[i] == -INFINITY ? -INFINITY : -nm[i], ls[i]);
 #pragma unroll
     for (int c0 = 0; c0 < COLS; c0 += C::MC) {
       __syncthreads();  // the ring, and the rows before, are read

@@ -19,13 +19,25 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// The weights' common factor is 2^kMaxLw at most: sums of 2^31 weights of up to
-// 2^(kMaxLw + 8) stay in fp32's range.
-constexpr float kMaxLw = 60.f;
-// log2 of what a row's largest weight is brought to at least: the rest are kept to 2^-25, so
-// that even 2^15 of them, all rounded the same way, are off by 2^-12 of it. (Each power of two
-// more lets scales of half the size ask for the slow choice of the factor.)
-constexpr float kAimLw = 2.f;
+// How both forms keep a row's weights in fp16's range. All sums of a row hold p = 2^(score + n)
+// (scores in base 2); the value product's weights are p s, s the values' scales (or 2^e). n
+// follows the weights, not the scores: the first keys bring the largest p s to
+// 2^kWeightTop, n stands while p s <= 2^kWeightMost (a bound from the largest score and the
+// largest scale, both at hand, shows that), and then comes down to 2^kWeightTop again. So
+// the largest weight so far is 2^kWeightTop at least, and rounding small ones (to 2^-25) costs
+// 2^-30 of it: values of any sizes keep their precision beside one another. (With a factor
+// from the largest scale alone, one visible value of 2^20 times the others' and no
+// weight pushed their weights into the subnormals: errors of 1.6e-3, at 2^24 of 0.11.) p itself
+// is kept below 2^kPMost: sums of 2^31 of them, times zeros, stay in fp32's range.
+constexpr float kWeightTop = 5.f, kWeightMost = 14.f, kPTop = 60.f, kPMost = 64.f;
+// The new n of a row that sees keys: x its largest score, w log2 of its largest p s but for
+// n (-inf: none), first: no keys before.
+__device__ __forceinline__ float row_factor(float n, float x, float w, bool first) {
+  if (first || w + n > kWeightMost) n = kWeightTop - w;
+  return fminf(n, kPTop - x);
+}
+// floor(log2 x) of a float's bits (0: -127)
+__device__ __forceinline__ float log2_floor(uint32_t bits) { return float(int(bits >> 23) - 127); }
 __device__ __forceinline__ float half_lo(uint32_t m) {
   return __half2float(__ushort_as_half(uint16_t(m)));
 }

@@ -15,13 +15,13 @@
 //         rounds. (With z + 8 s and n - 8 the sum was rounded before it: the same for all
 //         channels of a group, which the inverse transform puts into one.)
 // Floor per 128 x 64 tile pair at d = 128: 3 x 256 cycles of the tensor cores (hi and
-// lo parts, values). Measured: 1024 queries x 32 heads over 9216 keys in 255 us at 1965 MHz
-// (574 TFLOP/s of the two products counted once) and in 280 at the 1815 MHz at which the
+// lo parts, values). Measured: 1024 queries x 32 heads over 9216 keys in 252 us at 1965 MHz
+// (580 TFLOP/s of the two products counted once) and in 277 at the 1815 MHz at which the
 // power cap holds a loop of such calls; 1660 cycles a tile, of which the
 // tensor cores are active for 770. A softmax works for most of its two tiles' time (two
 // softmax and two unpacking warps share an SM quarter's issue, 62% of it used), and
 // shared memory serves 840 wavefronts and the products' operands a tile. With two groups
-// 321 us, with four 459 us (two tiles' scores fit, and more fused multiplies).
+// 322 us, with four 467 us (two tiles' scores fit, and more fused multiplies).
 //
 // Warps 0..3 do the even tiles' softmax, 4..7 the odd ones', a thread per row with a
 // maximum, a sum and an output accumulator of its own: the two never wait for each other,
@@ -816,10 +816,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       tm_fence_before();  // (the segment before has been read)
       __syncwarp();
       if (lane == 0) mbar_arrive(qready);
-      // Running state as in kvc_cache_attend.cuh, with 2^(a value's e) for its scale s: weights
-      // 2^(nm + score + e) reach up to 2^15; nm = lw - m. lw is chosen from the tile's e and the
-      // row's weights when m rises or a larger e comes.
-      float nm = 0.f, thr = -INFINITY, l = 0.f, lw = 0.f, v_most = 0.f;
+      // Running state as in kvc_cache_attend.cuh: n (row_factor), the sum of p. While raw scores
+      // stay below thr (-inf: none seen so far, or nothing but NaN) and the values' 2^e below
+      // v_most, no weight passes its range; both are those of the last tile that was not below.
+      float nm = 0.f, thr = -INFINITY, l = 0.f, v_most = 0.f;
       float *taint = reinterpret_cast<float *>(smem + C::taint) + which * kPfRows + row;
       *taint = 0.f;  // NaN once the row has seen a value that is not finite
 
@@ -882,49 +882,38 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
         const float4 wm = *reinterpret_cast<const float4 *>(smem + C::wmax + buf * 16);
         const float vm = fmaxf(fmaxf(wm.x, wm.y), fmaxf(wm.z, wm.w));
-        if (__any_sync(0xFFFFFFFFu, top > thr || vm > v_most)) {
-          const float x = top * fc;
-          const float was = lw - nm;
-          float now = was, most = kMaxLw;  // m; what lw may be
-          if (thr == -INFINITY) {  // nothing but NaN so far, if anything
-            if (top > -INFINITY) now = x;
-          } else {
-            const float rise = top > thr ? x - now : 0.f;
-            if (v_most != 0.f) most = fminf(most, lw + rise);
-            now += rise;
-          }
-          const bool any = thr != -INFINITY || top > -INFINITY;
-          // the smallest e but zeros' (0: zeros alone)
-          const uint32_t *vb = reinterpret_cast<const uint32_t *>(meta) + 2 * NG * NK;
-          uint32_t low = (vb[lane] & 0x7FFFFFFFu) - 1u;
-          if constexpr (NK == 64) low = min(low, (vb[lane + 32] & 0x7FFFFFFFu) - 1u);
-          low = (__reduce_min_sync(0xFFFFFFFFu, low) + 1u) >> 23;
-          float lnew = lw;
-          if (vm != 0.f || v_most != 0.f) {
-            const float least = vm == 0.f ? -INFINITY : float(132 - int(__float_as_uint(vm) >> 23));  // 5 - e
-            // m + log2 of the largest weight; where the e are so much alike that `least` is
-            // the larger choice for sure, the largest score with the smallest e does
-            float big = x + float(int(low) - 127);
-            if (low == 0u || now + kAimLw - big > least) {
-              big = -INFINITY;
+        if (__any_sync(0xFFFFFFFFu, top > thr) || vm > v_most) {
+          const float e_top = log2_floor(__float_as_uint(vm)), x = top * fc;
+          v_most = 4.f * vm;
+          const bool first = thr == -INFINITY;
+          float fac = 1.f;
+          const float most = fminf(kPMost, kWeightMost - 1.f - e_top);
+          const bool need = x > -INFINITY && (first || x + nm > most);
+          if (__any_sync(0xFFFFFFFFu, need)) {
+            // the smallest e but zeros' (0: zeros alone)
+            const uint32_t *vb = reinterpret_cast<const uint32_t *>(meta) + 2 * NG * NK;
+            uint32_t low = (vb[lane] & 0x7FFFFFFFu) - 1u;
+            if constexpr (NK == 64) low = min(low, (vb[lane + 32] & 0x7FFFFFFFu) - 1u);
+            low = __reduce_min_sync(0xFFFFFFFFu, low) + 1u;
+            float w = x + e_top + 1.f;  // (where the e are alike, it will do)
+            if (low == 0u || e_top - log2_floor(low) > 3.f) {
+              w = -INFINITY;
 #pragma unroll
               for (int y = 0; y < NK; y += 4) {
                 const uint4 ev = *reinterpret_cast<const uint4 *>(meta + 2 * NG * NK + y);
                 auto at = [&](float x, uint32_t u) {  // x fc + e (zeros: -127)
                   return fmaf(x, fc, __uint_as_float(((u >> 23) & 255u) | 0x4B000000u) - 8388735.f);
                 };
-                big = max3(max3(big, at(sc[y], ev.x), at(sc[y + 1], ev.y)), at(sc[y + 2], ev.z), at(sc[y + 3], ev.w));
+                w = max3(max3(w, at(sc[y], ev.x), at(sc[y + 1], ev.y)), at(sc[y + 2], ev.z), at(sc[y + 3], ev.w));
               }
             }
-            if (any) lnew = fmaxf(least, fminf(most, now + kAimLw - big));
-            else if (vm != 0.f) lnew = least;
-            v_most = ex2(7.f - lnew);
+            if (need) {
+              const float n = row_factor(nm, x, w, first);
+              if (!first) fac = ex2(n - nm);
+              nm = n;
+            }
           }
-          const float n = lnew == lw && now == was ? nm : lnew - now;
-          const float fac = thr == -INFINITY ? 1.f : ex2(n - nm);
-          if (any) thr = (now + 8.f) / fc;
-          nm = n;
-          lw = lnew;
+          if (!first || x > -INFINITY) thr = (most - nm) / fc;
           l *= fac;
           if (i > 1 && __any_sync(0xFFFFFFFFu, fac != 1.f)) {  // this softmax's last values are in
             pf_wait(pv + (j - 2) % kPfStages, ((j - 2) / kPfStages) & 1u, dead, a.status);

@@ -583,8 +583,8 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
         }
         if (__any_sync(0xFFFFFFFFu, raise)) {
           float fac[R];
-          // The largest and the smallest scale but zeros: where they are alike, the largest score
-          // with the largest scale will do for the largest weight.
+          // The largest and the smallest scale: where they are alike, the largest score with the
+          // largest scale will do for the largest weight.
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xFFFFFFFFu, smax, o));
           uint32_t low = ~0u;
@@ -592,10 +592,10 @@ __global__ void __launch_bounds__(CaCfg<D, G, NB>::THREADS, CaCfg<D, G, NB>::CTA
           for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int gg = 0; gg < NG; ++gg)
-              low = min(low, min((vA[x][gg] & 0x7FFFu) - 1u, (vB[x][gg] & 0x7FFFu) - 1u));
-          low = __reduce_min_sync(0xFFFFFFFFu, low) + 1u;
+              low = min(low, min(vA[x][gg] & 0x7FFFu, vB[x][gg] & 0x7FFFu));
+          low = __reduce_min_sync(0xFFFFFFFFu, low);
           const float e_top = log2_floor(__float_as_uint(fminf(smax, 65504.f)));
-          const bool look = low == 0u || e_top - log2_floor(__float_as_uint(half_lo(low))) > 3.f;
+          const bool look = e_top - log2_floor(__float_as_uint(half_lo(low))) > 3.f;
 #pragma unroll
           for (int i = 0; i < R; ++i) {
             float x = top[i];

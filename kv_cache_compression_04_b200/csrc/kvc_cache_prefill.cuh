@@ -890,13 +890,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           const float most = fminf(kPMost, kWeightMost - 1.f - e_top);
           const bool need = x > -INFINITY && (first || x + nm > most);
           if (__any_sync(0xFFFFFFFFu, need)) {
-            // the smallest e but zeros' (0: zeros alone)
+            // the smallest e (of zeros and keys that are not there: -127)
             const uint32_t *vb = reinterpret_cast<const uint32_t *>(meta) + 2 * NG * NK;
-            uint32_t low = (vb[lane] & 0x7FFFFFFFu) - 1u;
-            if constexpr (NK == 64) low = min(low, (vb[lane + 32] & 0x7FFFFFFFu) - 1u);
-            low = __reduce_min_sync(0xFFFFFFFFu, low) + 1u;
+            uint32_t low = vb[lane] & 0x7FFFFFFFu;
+            if constexpr (NK == 64) low = min(low, vb[lane + 32] & 0x7FFFFFFFu);
+            low = __reduce_min_sync(0xFFFFFFFFu, low);
             float w = x + e_top + 1.f;  // (where the e are alike, it will do)
-            if (low == 0u || e_top - log2_floor(low) > 3.f) {
+            if (e_top - log2_floor(low) > 3.f) {
               w = -INFINITY;
 #pragma unroll
               for (int y = 0; y < NK; y += 4) {

@@ -304,3 +304,32 @@ def test_values_of_very_different_sizes_in_long_segments(kind, d, g, qpk, asked)
     got = out.double().cpu().numpy().reshape(L, R, asked, H, qpk, d)
     bad = np.abs(got - o[0][None, None, :, None]) - tol[0][None, None, :, None]
     assert (bad <= 0).all(), bad.max()
+
+
+@pytest.mark.parametrize("d,g", [(128, 128), (128, 32), (64, 64)])
+@pytest.mark.parametrize("asked", [1, 2, 9, 60])
+@pytest.mark.parametrize("n,at", [(192, 70), (192, 0), (190, 185)])
+def test_a_zero_value_with_nearly_all_the_weight(d, g, asked, n, at):
+    """One key's score is 17 above the others', its value zeros: what is left keeps its
+    precision, though the values beside it are all alike."""
+    qpk, rng = 4, np.random.default_rng(d + at)
+    c = make(d, g, 1, 1, 13, 16)
+    u = rng.standard_normal(d)
+    score = rng.uniform(-0.5, 0.5, n)
+    score[at] = 17
+    k, v = score[:, None] * u / (u @ u) * d ** 0.5, rng.standard_normal((n, d)) * 2.0 ** 6
+    v[at] = 0
+    c.write(ref.bf16(k)[None, :, None].cuda(), ref.bf16(v)[None, :, None].cuda(), torch.arange(n, device="cuda"))
+    q = torch.from_numpy(u + 0.02 * rng.standard_normal((1, asked, qpk, d))).to(torch.bfloat16).cuda()
+    out = c.attend(q, torch.arange(12, dtype=torch.int32, device="cuda")[None], dev([n]),
+                   q_starts=dev([0, asked]), max_q=asked) * 2.0 ** 12
+    c.check()
+    x, spread = cache_values(c, np.arange(n))
+    x[:, 1] *= 2.0 ** 12
+    spread[:, 1] *= 2.0 ** 12
+    o, _, mag, size = ref.attend(x, q.double().cpu().numpy(), qpk, d ** -0.5,
+                                 [(0, n - asked + i + 1) for i in range(asked)], spread)
+    ds = 2.0 ** -18 * size + 2.0 ** -20
+    tol = 2.0 ** -8 * np.abs(o) + (2 * ds + 2.0 ** -11)[..., None] * mag * 1.01 + 1e-7
+    bad = np.abs(out.double().cpu().numpy() - o) - tol
+    assert (bad <= 0).all(), bad.max()

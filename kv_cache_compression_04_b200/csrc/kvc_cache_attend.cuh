@@ -24,7 +24,7 @@
 // either, the warp-level product is an emulation: 60% slower in all.) Queries are split
 // in fp16 hi + lo (22 bits). The eight columns are eight query rows, the score
 // product taking both parts into one sum; the value product's weights are rounded to
-// fp16 once (2^-11 relative at most, independent per key, and 2^-30 of the row's largest
+// fp16 once (2^-11 relative at most, independent per key, and 2^-26 of the row's largest
 // weight for small ones: no more than rounding the output to fp16). Up to 4 rows, columns
 // 2 i, 2 i + 1 are row i's two parts in both products.
 //

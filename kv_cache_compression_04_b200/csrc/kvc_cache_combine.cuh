@@ -23,9 +23,10 @@ __device__ __forceinline__ float lg2(float x) {
 // (scores in base 2); the value product's weights are p s, s the values' scales (or 2^e). n
 // follows the weights, not the scores: the first keys bring the largest p s to
 // 2^kWeightTop, n stands while p s <= 2^kWeightMost (a bound from the largest score and the
-// largest scale, both at hand, shows that), and then comes down to 2^kWeightTop again. So
-// the largest weight so far is 2^kWeightTop at least, and rounding small ones (to 2^-25) costs
-// 2^-30 of it: values of any sizes keep their precision beside one another. (With a factor
+// largest scale, both at hand, shows that), and then comes down to 2^kWeightTop again. Where a
+// tile's scales lie within 2^3, the largest score and scale stand for the largest p s. So
+// the largest weight so far is 2 at least, and rounding small ones (to 2^-25) costs
+// 2^-26 of it: values of any sizes keep their precision beside one another. (With a factor
 // from the largest scale alone, one visible value of 2^20 times the others' and no
 // weight pushed their weights into the subnormals: errors of 1.6e-3, at 2^24 of 0.11.) p itself
 // is kept below 2^kPMost: sums of 2^31 of them, times zeros, stay in fp32's range.

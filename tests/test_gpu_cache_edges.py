@@ -333,3 +333,25 @@ def test_a_zero_value_with_nearly_all_the_weight(d, g, asked, n, at):
     tol = 2.0 ** -8 * np.abs(o) + (2 * ds + 2.0 ** -11)[..., None] * mag * 1.01 + 1e-7
     bad = np.abs(out.double().cpu().numpy() - o) - tol
     assert (bad <= 0).all(), bad.max()
+
+
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -9, 2.0 ** -18, 0.0])
+@pytest.mark.parametrize("d,g,qpk,asked", [(128, 128, 4, 1), (128, 32, 8, 1), (64, 64, 4, 8), (128, 64, 4, 40)])
+def test_lse_keeps_its_precision_whatever_the_values_are(d, g, qpk, asked, size):
+    """lse against 64 bits, with values of any size and none: the scores' bound and a
+    rounding or two of lse itself."""
+    n, rng = 150, np.random.default_rng(3)
+    c = make(d, g, 1, 1, 11, 16)
+    k, v = rows(1, n, 1, d)
+    k = k * 0.25  # small scores: lse is near ln n, and the scores' bound small
+    c.write(k, v * size, torch.arange(n, device="cuda"))
+    q = torch.from_numpy(rng.standard_normal((1, asked, qpk, d)) * 0.25).to(torch.bfloat16)
+    lse = torch.empty(q.shape[:3], device="cuda")
+    c.attend(q.cuda(), torch.arange(10, dtype=torch.int32, device="cuda")[None], dev([n]),
+             q_starts=dev([0, asked]), max_q=asked, lse=lse)
+    c.check()
+    x, spread = cache_values(c, np.arange(n))
+    _, l, _, s = ref.attend(x, q.double().numpy(), qpk, d ** -0.5, [(0, n - asked + i + 1) for i in range(asked)], spread)
+    # the sum of n exponentials, each off by exp2's 2^-22 and its argument's rounding (2^-24 of at
+    # most 64): 2^-18 in all; two roundings of a result below 8
+    assert (np.abs(lse.double().cpu().numpy() - l) <= 2.0 ** -18 * s + 2.0 ** -18 + 2.0 ** -21).all()

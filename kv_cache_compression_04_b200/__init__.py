@@ -548,6 +548,15 @@ class PagedCache:
             raise ValueError(f"the stream is on device {stream.device_index}, the cache on {self.device}")
         return stream.cuda_stream
 
+    def _may_wait(self, stream, where: str):
+        """Waiting for a stream that is being captured would end the capture."""
+        import torch
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self._may_wait(None, where)
+        if torch._C._cuda_isCurrentStreamCapturing():
+            raise ValueError(f"{where} waits, which a stream that is being captured cannot")
+
     def _workspace(self, stream, handle: int, nbytes):
         """The stream's workspace if it has nbytes() (called where that has to be known; 0 for
         arguments that the call then refuses, which no null pointer may hide)."""
@@ -638,6 +647,8 @@ class PagedCache:
                 not stream_buf.is_contiguous():
             raise ValueError("stream_buf: expects a contiguous uint8 buffer of nbytes")
         s = self._here(stream, stream_buf, slots)
+        if check:
+            self._may_wait(stream, "load(check=True)")
         n = len(seq_lens)
         seq, L, D = (C.c_int32 * (n or 1))(*map(int, seq_lens)), lib(), C.byref(self.desc)
         self._with_workspace(
@@ -697,6 +708,7 @@ class PagedCache:
         """Waits for the stream, raises the first data-dependent error since the last
         check, and clears it."""
         s = self._here(stream)
+        self._may_wait(stream, "check()")
         st = kvc_stream_status(self._status, s)
         if st != KVC_OK:
             kvc_cache_status_clear(self._status, s)

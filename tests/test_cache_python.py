@@ -86,3 +86,15 @@ def test_attention_of_too_many_rows_is_refused():
                                    n * 4096, 4096, 128, fake, n * 4096, 4096, 128, None)
             assert (kvc.kvc_cache_attend_workspace_bytes(c, t) == 0) == (n == tokens)
             assert kvc.kvc_cache_attend(c, t, fake, 1 << 60, None, None) == want
+
+
+def test_waiting_calls_refuse_a_capture(monkeypatch):
+    """Before anything is enqueued, on the current stream and on one that is given."""
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: True)
+    c = HostCache()
+    for stream in (None, object()):
+        with pytest.raises(ValueError):
+            c.check(stream=stream)
+        with pytest.raises(ValueError):
+            c.load(torch.zeros(64, dtype=torch.uint8), 64, torch.zeros(5, dtype=torch.int64), [5], stream=stream, check=True)
+    assert status(lambda: load(c, [5])) == ENQUEUED and not c._ws

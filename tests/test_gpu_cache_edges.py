@@ -355,3 +355,25 @@ def test_lse_keeps_its_precision_whatever_the_values_are(d, g, qpk, asked, size)
     # the sum of n exponentials, each off by exp2's 2^-22 and its argument's rounding (2^-24 of at
     # most 64): 2^-18 in all; two roundings of a result below 8
     assert (np.abs(lse.double().cpu().numpy() - l) <= 2.0 ** -18 * s + 2.0 ** -18 + 2.0 ** -21).all()
+
+
+def test_waiting_calls_leave_a_capture_alone():
+    """check() and load(check=True) wait: under capture they refuse, and the graph goes on."""
+    d, g, L, H, T = 64, 64, 1, 2, 50
+    kv = torch.randn(L, 2, H, T, d, device="cuda").to(torch.bfloat16)
+    buf, n, back = stream_of(kv, g, 11, 0, 0, 0)
+    c = make(d, g, L, H, 6, 16)
+    at = torch.from_numpy(slots_for(T, 6, 16)).cuda()
+    c.load(buf, n, at, [T], check=True)
+    c.pool.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError):
+            c.load(buf, n, at, [T], check=True)
+        with pytest.raises(ValueError):
+            c.check()
+        c.load(buf, n, at, [T])
+    graph.replay()
+    c.check()
+    k, v = c.read(at)
+    assert torch.equal(k.transpose(1, 2), back[:, 0]) and torch.equal(v.transpose(1, 2), back[:, 1])

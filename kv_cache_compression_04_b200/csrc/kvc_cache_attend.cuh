@@ -46,10 +46,10 @@
 // (1088 to 1280 bytes, as 16-token pages allow) took about 70 cycles each of an SM's
 // copy engine, four of them a chunk, where 32 tokens should take 200 in all.
 //
-// Measured: 64 ragged requests up to 8192 keys, 64 / 8 heads, two groups: 91 us for the
-// second kernel against 47 for the bytes, at 376 warp instructions per tile and head and
+// Measured: 64 ragged requests up to 8192 keys, 64 / 8 heads, two groups: 89 us for the
+// second kernel against 47 for the bytes, at 374 warp instructions per tile and head and
 // 2.3 issued per cycle (what bounds it; 2 of 3 are the codes' conversion, addresses and
-// softmax). One request of 131072 keys, four groups: 35 us. One of 4096: 9 us of which
+// softmax). One request of 131072 keys, four groups: 34 us. One of 4096: 9 us of which
 // the chunk itself takes 1; the kernels before and after it take 4 and 6.
 //
 // Three kernels: the first reads the requests' numbers, checks them, and turns each

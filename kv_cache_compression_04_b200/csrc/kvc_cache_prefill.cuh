@@ -21,7 +21,7 @@
 // tensor cores are active for 770. A softmax works for most of its two tiles' time (two
 // softmax and two unpacking warps share an SM quarter's issue, 62% of it used), and
 // shared memory serves 840 wavefronts and the products' operands a tile. With two groups
-// 322 us, with four 467 us (two tiles' scores fit, and more fused multiplies).
+// 322 us, with four 469 us (two tiles' scores fit, and more fused multiplies).
 //
 // Warps 0..3 do the even tiles' softmax, 4..7 the odd ones', a thread per row with a
 // maximum, a sum and an output accumulator of its own: the two never wait for each other,
